@@ -236,6 +236,140 @@ int mxq_linear_noalloc(const void* x_bf16, const void* W_q, const uint8_t* W_sf,
                        const float* g_A, int64_t M, int64_t N, int64_t K, mxq_fmt fmt, mxq_rule act_rule,
                        mxq_out out_type, void* out, mxq_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------------------------------
+ * A paged key/value cache held in 4 bits (MXFP4 or NVFP4), and attention over it.  The pages name no
+ * such cache; its blocks, scales and rounding are those of mxq_quantize along the head dimension.
+ *
+ * One layer of the cache is num_pages pages of page_size tokens (a multiple of 16, at most 1024) for
+ * kv_heads heads of head_dim D (64, 128 or 256) elements:
+ *   uint8 [num_pages][kv_heads][page_size / 16][unit],  unit = mxq_kv_unit_bytes(D, fmt) bytes.
+ * A unit holds 16 tokens of one head as  K codes (8 D bytes) | V codes (8 D) | K scales | V scales, with
+ * nb = D / 32 (MXFP4) or D / 16 (NVFP4) scale bytes a token and side.  "Row bytes" are a token's D / 2
+ * bytes of codes, byte i = elements 2i (low nibble) and 2i + 1.
+ *   K codes   dealt to four quarters t of D / 8 bytes: NVFP4 quarter t is row bytes [t D/8, (t+1) D/8);
+ *             MXFP4 quarter t is the row's 32-bit words t, t + 4, t + 8, ...  Quarters are cut in pieces
+ *             of min(16, D / 8) bytes, stored [piece][token][t].
+ *   V codes   row byte 8 j + g of a token is byte (token % 2) D/16 + j of the D/8-byte record of lane
+ *             4 g + (token % 8) / 2 of the token's group of eight; records are cut in pieces of
+ *             min(16, D / 8) bytes, stored [token / 8][piece][lane].
+ *   K scales  [token][nb].     V scales  [token / 2][nb][token % 2].
+ * A slot is page * page_size + offset, the place of one token; num_pages * page_size < 2^31.
+ * Sequence b's token p lies in page block_table[b][p / page_size].
+ * The kernels check what they read on the device before they use it as an index.  What they find out of
+ * range is skipped and recorded in the device status word (mxq_device_status), first finding first:
+ * 0x200 a slot, 0x201 a page of the block table, 0x202 q_start, 0x203 a length the table cannot hold.
+ */
+
+/* Bytes of one unit (16 tokens of one head). */
+int mxq_kv_unit_bytes(int head_dim, mxq_fmt fmt, size_t* bytes);
+
+/*
+ * Quantize tokens into the cache: k, v [tokens, kv_heads, D] bf16 (device; element strides k_token_stride
+ * and so on, multiples of 8, the innermost dimension contiguous) go to slots[i] (device int32; negative:
+ * the token is skipped).  Blocks along D, rule and global scales as in mxq_quantize; g_k, g_v (device)
+ * fp32[1] for NVFP4.  Bytes of other tokens are left as they are.  Slots of one call are distinct; where
+ * two are not, their place receives a mixture of both tokens.  tokens = 0 does nothing.
+ */
+int mxq_kv_append(const void* k, const void* v, int64_t tokens, int kv_heads, int head_dim, int64_t k_token_stride,
+                  int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                  mxq_fmt fmt, mxq_rule rule, const float* g_k, const float* g_v, void* cache, int64_t num_pages,
+                  int page_size, mxq_stream_t stream);
+
+/*
+ * Read tokens back as bf16: k_out, v_out [tokens, kv_heads, D] (device, contiguous) receive the values
+ * that mxq_fake_quantize gives for what was appended at slots[i] (negative or out of range: zeros).
+ */
+int mxq_kv_read(const void* cache, int64_t num_pages, int page_size, int kv_heads, int head_dim, mxq_fmt fmt,
+                const int32_t* slots, int64_t tokens, const float* g_k, const float* g_v, void* k_out, void* v_out,
+                mxq_stream_t stream);
+
+/* Workspace bytes of mxq_kv_attention on the current device (0 for arguments it refuses). */
+size_t mxq_kv_attention_workspace_size(int64_t batch, int64_t max_q, int heads, int kv_heads, int head_dim);
+
+/*
+ * Attention over the cache: out[i] = sum_p w_ip V_p with w_i = softmax over the visible tokens p of
+ * scale * q_i . K_p, for heads = kv_heads * group query heads (head h reads kv head h / group).
+ *   q            (device) [rows, heads, D] bf16; element strides q_token_stride, q_head_stride, multiples
+ *                of 8; the innermost dimension contiguous.
+ *   block_table  (device) int32 [batch][table_stride], the first max_pages columns used; entries behind a
+ *                sequence's last page are not read.  kv_lens (device) int32 [batch]: tokens in the cache,
+ *                the query tokens' own included.
+ *   q_start      (device) int32 [batch + 1]: sequence b's query rows are q_start[b] .. q_start[b + 1] - 1,
+ *                at most max_q; NULL: max_q rows each, rows = batch * max_q.
+ *   causal       query j of a sequence's n sees the tokens up to its own, kv_lens[b] - n + j; 0: all.
+ *   window       > 0: only the last `window` of the tokens up to its own; 0: no limit.
+ *   g_k, g_v     (device) fp32[1] NVFP4 global scales; ignored (may be NULL) for MXFP4.
+ *   out          (device) [rows, heads, D] bf16 (RNE) or fp32.  lse (device) fp32 [rows, heads], the natural
+ *                logarithm of the softmax's denominator, or NULL.  A row that sees no token gets zeros and
+ *                -inf.  Rows of no sequence are left as they were.
+ *   workspace    (device) at least mxq_kv_attention_workspace_size(...) bytes; needs no preparation.
+ * fp32 softmax and sums; probabilities are rounded to f16 (11 bits) for the product with V.  MXFP4 blocks
+ * of V whose scale is 2^23 or more below the largest in the same 32 channels (over the tokens that one
+ * warp takes) count as zero.  Results do not depend on timing.  Two launches.  Calls that may run at the
+ * same time need a workspace each.
+ */
+int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
+                     int64_t num_pages, int page_size, int heads, int kv_heads, int head_dim, mxq_fmt fmt,
+                     const int32_t* block_table, int64_t table_stride, int64_t max_pages, const int32_t* kv_lens,
+                     int64_t batch, const int32_t* q_start, int64_t max_q, float scale, int causal, int64_t window,
+                     const float* g_k, const float* g_v, mxq_out out_type, void* out, float* lse, void* workspace,
+                     size_t ws_bytes, mxq_stream_t stream);
+
+/*
+ * Page bookkeeping.  The state lies on the device: block_table int32 [table_rows][table_stride] (max_pages
+ * columns used, -1 where a sequence has no page), kv_lens int32 [table_rows], refs int32 [num_pages] (how
+ * many sequences hold a page; 0: free).  A call names n (at most MXQ_KV_MAX_SEQS) different rows
+ * (at most MXQ_KV_MAX_TABLE) and does all of its work or none:
+ *   info (device) int32[2]  info[0] = 0, or -1: a row outside the table, named twice or in an unfit state,
+ *                           -2: a count or length that is negative or too long, -3: not enough free pages;
+ *                           info[1] = the pages concerned (0 if refused).
+ * Calls are stream-ordered and may be captured into a graph; n = 0 does nothing.
+ */
+#define MXQ_KV_MAX_SEQS 4096
+#define MXQ_KV_MAX_TABLE 65536
+
+/*
+ * Room for add[i] more tokens in row seqs[i]: takes free pages, lowest index first in the order of the
+ * call's rows, and adds to kv_lens.  A last page that is not full and held by several rows is copied
+ * first, in all layers, so that the others keep their tokens.  The cache is `layers` layers of
+ * page_bytes = kv_heads * page_size / 16 * unit bytes a page, layer_stride bytes apart.
+ *   slots  (device) int32 [slots_cap] or NULL: the slots of the new tokens, row after row, then -1.
+ *   workspace (device) mxq_kv_reserve_workspace_size(n) bytes.   info[1] = pages taken.
+ */
+size_t mxq_kv_reserve_workspace_size(int64_t n);
+int mxq_kv_reserve(const int32_t* seqs, const int32_t* add, int64_t n, int32_t* block_table, int64_t table_rows,
+                   int64_t table_stride, int64_t max_pages, int32_t* kv_lens, int32_t* refs, int64_t num_pages,
+                   int page_size, void* cache, int64_t layers, int64_t layer_stride, int64_t page_bytes, int32_t* slots,
+                   int64_t slots_cap, int32_t* info, void* workspace, size_t ws_bytes, mxq_stream_t stream);
+
+/*
+ * Row children[i], which must be empty, becomes a copy of row parents[i] that shares all of its pages.  A
+ * row may be the parent of many, but not a parent and a child.  info[1] = page references added.
+ */
+int mxq_kv_fork(const int32_t* parents, const int32_t* children, int64_t n, int32_t* block_table, int64_t table_rows,
+                int64_t table_stride, int64_t max_pages, int32_t* kv_lens, int32_t* refs, int64_t num_pages,
+                int page_size, int32_t* info, mxq_stream_t stream);
+
+/*
+ * Cut row seqs[i] to new_lens[i] tokens (0: free it); pages that it no longer needs lose a reference and
+ * their table entries become -1.  info[1] = page references dropped.
+ */
+int mxq_kv_truncate(const int32_t* seqs, const int32_t* new_lens, int64_t n, int32_t* block_table, int64_t table_rows,
+                    int64_t table_stride, int64_t max_pages, int32_t* kv_lens, int32_t* refs, int64_t num_pages,
+                    int page_size, int32_t* info, mxq_stream_t stream);
+
+/*
+ * Pack the pages in use into [0, live): the i-th page in use at or behind `live` moves, in all layers, into
+ * the i-th free page in front of it; refs and the first ceil(kv_lens / page_size) entries of every table row
+ * follow.  workspace (device) mxq_kv_compact_workspace_size(num_pages) bytes.   info[1] = live.
+ */
+size_t mxq_kv_compact_workspace_size(int64_t num_pages);
+int mxq_kv_compact(int32_t* block_table, int64_t table_rows, int64_t table_stride, int64_t max_pages,
+                   const int32_t* kv_lens, int32_t* refs, int64_t num_pages, int page_size, void* cache, int64_t layers,
+                   int64_t layer_stride, int64_t page_bytes, int32_t* info, void* workspace, size_t ws_bytes,
+                   mxq_stream_t stream);
+
 /* Read the device status word that kernels set when a bounded wait gives up (0 = clean).
  * Synchronizes `stream`.  If reset != 0 the word is cleared afterwards. */
 int mxq_device_status(int* status_out, int reset, mxq_stream_t stream);

@@ -5,6 +5,7 @@ handle).  The tensor helpers below only allocate outputs with torch and marshal 
 step of the computation runs in the library's kernels.  There is no fallback: if the library is
 missing or the device is not an sm_100 part, the calls raise.
 """
+import contextlib
 import ctypes
 import os
 
@@ -41,6 +42,19 @@ SIGNATURES = {
     "mxq_linear_kernel_count": (_I, [_I64, _I64, _I64, _I]),
     "mxq_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _SZ, _P, _P]),
     "mxq_linear_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _P]),
+    "mxq_kv_unit_bytes": (_I, [_I, _I, ctypes.POINTER(_SZ)]),
+    "mxq_kv_append": (_I, [_P, _P, _I64, _I, _I, _I64, _I64, _I64, _I64, _P, _I, _I, _P, _P, _P, _I64, _I, _P]),
+    "mxq_kv_read": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P]),
+    "mxq_kv_attention_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I]),
+    "mxq_kv_attention": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I, _I, _I, _I, _I, _P, _I64, _I64, _P, _I64, _P, _I64,
+                              ctypes.c_float, _I, _I64, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "mxq_kv_reserve_workspace_size": (_SZ, [_I64]),
+    "mxq_kv_reserve": (_I, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _I64, _P, _P,
+                            _SZ, _P]),
+    "mxq_kv_fork": (_I, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I, _P, _P]),
+    "mxq_kv_truncate": (_I, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I, _P, _P]),
+    "mxq_kv_compact_workspace_size": (_SZ, [_I64]),
+    "mxq_kv_compact": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     "mxq_device_status": (_I, [ctypes.POINTER(_I), _I, _P]),
     "mxq_selftest_timeout": (_I, [_U64, _P]),
     "mxq_strerror": (ctypes.c_char_p, [_I]),
@@ -341,3 +355,252 @@ def linear(x, W_q, W_sf, N, fmt, act_rule=CEIL, out_dtype=torch.bfloat16, g_W=No
                       _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _stream(stream)),
            "mxq_linear")
     return out
+
+
+# ---------------------------------------------------------------- 4-bit key/value cache
+
+def kv_unit_bytes(head_dim, fmt):
+    """Bytes of a unit of the cache: 16 tokens of one head, keys and values."""
+    n = ctypes.c_size_t(0)
+    _check(lib().mxq_kv_unit_bytes(head_dim, _fmt(fmt), ctypes.byref(n)), "mxq_kv_unit_bytes")
+    return n.value
+
+
+def kv_cache_shape(num_pages, kv_heads, head_dim, fmt, page_size, layers=None):
+    """Shape of the uint8 tensor that holds one layer of the cache (or `layers` of them)."""
+    if page_size % 16:
+        raise MxqBufferError("page_size must be a multiple of 16 (got %d)" % page_size)
+    shape = (num_pages, kv_heads, page_size // 16, kv_unit_bytes(head_dim, fmt))
+    return shape if layers is None else (layers,) + shape
+
+
+def _same_device(first, **others):
+    """All tensors of a call lie on one device; it need not be the current one (see _on)."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, first.device))
+
+
+def _on(t):
+    """The call's launches go to the device of its tensors, on that device's current stream by default."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+
+
+def _need_ints(t, name, n=None):
+    if t is None:
+        return
+    if t.dtype != torch.int32:
+        raise MxqBufferError("%s must be torch.int32 (got %s)" % (name, t.dtype))
+    if n is not None and t.numel() < n:
+        raise MxqBufferError("%s holds %d values, the call needs %d" % (name, t.numel(), n))
+
+
+def _strided(t, name, heads=None, dim=None):
+    """[tokens, heads, dim] bf16 whose last dimension is contiguous: (token stride, head stride) in elements."""
+    if t.dtype != torch.bfloat16:
+        raise MxqBufferError("%s must be torch.bfloat16 (got %s)" % (name, t.dtype))
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise MxqBufferError("%s must be [tokens, heads, dim] as the cache has them (got %s)" % (name, tuple(t.shape)))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise MxqBufferError("%s needs a contiguous last dimension" % name)
+    # the stride of a dimension of one entry (or of none) is never used
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+
+
+def _ptr_strided(t):
+    if not t.is_cuda:
+        raise ValueError("mxq works on CUDA tensors only (got a %s tensor)" % t.device)
+    return t.data_ptr()
+
+
+def _kv_layer(cache, head_dim, f):
+    """(pages, kv_heads, page_size) of one layer of the cache."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4:
+        raise MxqBufferError("cache must be uint8 [pages, kv_heads, page_size / 16, unit] (got %s %s)" %
+                             (cache.dtype, tuple(cache.shape)))
+    unit = kv_unit_bytes(head_dim, f)
+    if cache.shape[3] != unit:
+        raise MxqBufferError("a unit of the cache holds %d bytes, heads of %d take %d" % (cache.shape[3], head_dim, unit))
+    return cache.shape[0], cache.shape[1], 16 * cache.shape[2]
+
+
+def kv_append(k, v, cache, slots, fmt, rule=CEIL, g_k=None, g_v=None, stream=None):
+    """Quantize k, v [tokens, kv_heads, dim] bf16 (strided) into one layer of the cache at `slots` (int32,
+    page * page_size + offset; negative: skipped)."""
+    f = _fmt(fmt)
+    T, H, D = k.shape if k.dim() == 3 else (0, 0, 0)
+    ks = _strided(k, "k")
+    pages, heads, page_size = _kv_layer(cache, D, f)
+    if H != heads:
+        raise MxqBufferError("k has %d heads, the cache %d" % (H, heads))
+    vs = _strided(v, "v", H, D)
+    if v.shape[0] != T:
+        raise MxqBufferError("k and v hold %d and %d tokens" % (T, v.shape[0]))
+    _need_ints(slots, "slots", T)
+    _need(g_k, "g_k", 4, torch.float32)
+    _need(g_v, "g_v", 4, torch.float32)
+    _same_device(cache, k=k, v=v, slots=slots, g_k=g_k, g_v=g_v)
+    with _on(cache):
+        _check(lib().mxq_kv_append(_ptr_strided(k), _ptr_strided(v), T, H, D, ks[0], ks[1], vs[0], vs[1], _ptr(slots), f,
+                                   _rule(rule), _ptr(g_k), _ptr(g_v), _ptr(cache), pages, page_size, _stream(stream)),
+               "mxq_kv_append")
+
+
+def kv_read(cache, slots, fmt, head_dim, g_k=None, g_v=None, k_out=None, v_out=None, stream=None):
+    """The tokens at `slots` of one layer of the cache as bf16 (k, v), each [tokens, kv_heads, head_dim]."""
+    f = _fmt(fmt)
+    pages, H, page_size = _kv_layer(cache, head_dim, f)
+    _need_ints(slots, "slots")
+    T = slots.numel()
+    if k_out is None:
+        k_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+    _need(k_out, "k_out", 2 * T * H * head_dim, torch.bfloat16)
+    _need(v_out, "v_out", 2 * T * H * head_dim, torch.bfloat16)
+    _need(g_k, "g_k", 4, torch.float32)
+    _need(g_v, "g_v", 4, torch.float32)
+    _same_device(cache, slots=slots, k_out=k_out, v_out=v_out, g_k=g_k, g_v=g_v)
+    with _on(cache):
+        _check(lib().mxq_kv_read(_ptr(cache), pages, page_size, H, head_dim, f, _ptr(slots), T, _ptr(g_k), _ptr(g_v),
+                                 _ptr(k_out), _ptr(v_out), _stream(stream)), "mxq_kv_read")
+    return k_out, v_out
+
+
+def kv_attention_workspace(batch, max_q, heads, kv_heads, head_dim):
+    """Workspace bytes of kv_attention on the current device."""
+    return lib().mxq_kv_attention_workspace_size(batch, max_q, heads, kv_heads, head_dim)
+
+
+def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, scale=None, causal=True, window=0, g_k=None,
+                 g_v=None, out_dtype=torch.bfloat16, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q [rows, heads, dim] bf16 (strided) over one layer of the cache: (out [rows, heads, dim],
+    lse [rows, heads] fp32, natural logarithm).
+
+    block_table int32 [batch, pages], kv_lens int32 [batch] (the query tokens included), q_start int32
+    [batch + 1] (None: max_q rows a sequence).  scale: dim ** -0.5 by default.  Rows that see no token
+    get zeros and -inf; rows of no sequence are left as they were."""
+    f = _fmt(fmt)
+    rows, heads, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    qs = _strided(q, "q")
+    pages, kv_heads, page_size = _kv_layer(cache, D, f)
+    if block_table.dim() != 2 or (block_table.numel() and block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise MxqBufferError("block_table must be [batch, pages] with contiguous rows")
+    batch, cols = block_table.shape
+    _need_ints(block_table, "block_table")
+    _need_ints(kv_lens, "kv_lens", batch)
+    _need_ints(q_start, "q_start", batch + 1)
+    ot = OUT_FP32 if (out.dtype if out is not None else out_dtype) == torch.float32 else OUT_BF16
+    if out is None:
+        out = torch.empty((rows, heads, D), dtype=out_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+    _need(out, "out", rows * heads * D * (4 if ot == OUT_FP32 else 2), torch.float32 if ot == OUT_FP32 else torch.bfloat16)
+    _need(lse, "lse", 4 * rows * heads, torch.float32)
+    _need(g_k, "g_k", 4, torch.float32)
+    _need(g_v, "g_v", 4, torch.float32)
+    _same_device(q, cache=cache, block_table=block_table, kv_lens=kv_lens, q_start=q_start, g_k=g_k, g_v=g_v, out=out,
+                 lse=lse, workspace=workspace)
+    with _on(q):
+        if workspace is None:
+            workspace = torch.empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), dtype=torch.uint8,
+                                    device=q.device)
+        stride = block_table.stride(0) if batch > 1 else max(cols, 1)
+        _check(lib().mxq_kv_attention(_ptr_strided(q), rows, qs[0], qs[1], _ptr(cache), pages, page_size, heads, kv_heads, D,
+                                      f, _ptr_strided(block_table), stride, cols, _ptr(kv_lens), batch, _ptr(q_start),
+                                      max_q, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _ptr(g_k),
+                                      _ptr(g_v), ot, _ptr(out), _ptr(lse), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_attention")
+    return out, lse
+
+
+def _pages_state(block_table, kv_lens, refs, info):
+    """Checks the page state and returns (rows, stride, columns, info tensor)."""
+    if block_table.dim() != 2 or not block_table.is_contiguous():
+        raise MxqBufferError("block_table must be a contiguous [rows, pages] tensor")
+    _need_ints(block_table, "block_table")
+    _need_ints(kv_lens, "kv_lens", block_table.shape[0])
+    _need_ints(refs, "refs", 1)
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=refs.device)
+    _need_ints(info, "info", 2)
+    return block_table.shape[0], block_table.shape[1], info
+
+
+def _kv_layers(cache, page_size, num_pages):
+    """(layers, layer stride, bytes of a page) of a cache of one or more layers."""
+    if cache.dtype != torch.uint8 or cache.dim() not in (4, 5) or not cache.is_contiguous():
+        raise MxqBufferError("cache must be a contiguous uint8 [(layers,) pages, kv_heads, page_size / 16, unit] tensor")
+    layers = cache.shape[0] if cache.dim() == 5 else 1
+    pages, heads, units, unit = cache.shape[-4:]
+    if pages < num_pages or 16 * units != page_size:
+        raise MxqBufferError("the cache has %d pages of %d tokens, the call is for %d of %d" %
+                             (pages, 16 * units, num_pages, page_size))
+    return layers, pages * heads * units * unit, heads * units * unit
+
+
+def kv_reserve(seqs, add, block_table, kv_lens, refs, cache, page_size, slots=None, info=None, workspace=None, stream=None):
+    """Room for add[i] more tokens in row seqs[i] (int32 each); `cache` is [pages, ...] or [layers, pages, ...].
+    slots receives the new tokens' slots, then -1.  Returns info (int32[2]: status, pages taken)."""
+    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
+    n, num_pages = seqs.numel(), refs.numel()
+    _need_ints(seqs, "seqs")
+    _need_ints(add, "add", n)
+    _need_ints(slots, "slots")
+    layers, stride, page_bytes = _kv_layers(cache, page_size, num_pages)
+    _same_device(refs, seqs=seqs, add=add, block_table=block_table, kv_lens=kv_lens, cache=cache, slots=slots, info=info,
+                 workspace=workspace)
+    with _on(refs):
+        if workspace is None:
+            workspace = torch.empty(max(lib().mxq_kv_reserve_workspace_size(n), 16), dtype=torch.uint8, device=refs.device)
+        _check(lib().mxq_kv_reserve(_ptr(seqs), _ptr(add), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens), _ptr(refs),
+                                    num_pages, page_size, _ptr(cache), layers, stride, page_bytes, _ptr(slots),
+                                    0 if slots is None else slots.numel(), _ptr(info), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_reserve")
+    return info
+
+
+def kv_fork(parents, children, block_table, kv_lens, refs, page_size, info=None, stream=None):
+    """Empty row children[i] becomes a copy of row parents[i] that shares its pages.  Returns info."""
+    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
+    n = parents.numel()
+    _need_ints(parents, "parents")
+    _need_ints(children, "children", n)
+    _same_device(refs, parents=parents, children=children, block_table=block_table, kv_lens=kv_lens, info=info)
+    with _on(refs):
+        _check(lib().mxq_kv_fork(_ptr(parents), _ptr(children), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens),
+                                 _ptr(refs), refs.numel(), page_size, _ptr(info), _stream(stream)), "mxq_kv_fork")
+    return info
+
+
+def kv_truncate(seqs, new_lens, block_table, kv_lens, refs, page_size, info=None, stream=None):
+    """Cut row seqs[i] to new_lens[i] tokens (0 frees it).  Returns info."""
+    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
+    n = seqs.numel()
+    _need_ints(seqs, "seqs")
+    _need_ints(new_lens, "new_lens", n)
+    _same_device(refs, seqs=seqs, new_lens=new_lens, block_table=block_table, kv_lens=kv_lens, info=info)
+    with _on(refs):
+        _check(lib().mxq_kv_truncate(_ptr(seqs), _ptr(new_lens), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens),
+                                     _ptr(refs), refs.numel(), page_size, _ptr(info), _stream(stream)), "mxq_kv_truncate")
+    return info
+
+
+def kv_compact_workspace(num_pages):
+    """Workspace bytes of kv_compact."""
+    return lib().mxq_kv_compact_workspace_size(num_pages)
+
+
+def kv_compact(block_table, kv_lens, refs, cache, page_size, info=None, workspace=None, stream=None):
+    """Pack the pages in use to the front of the cache.  Returns info (int32[2]: 0, pages in use)."""
+    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
+    num_pages = refs.numel()
+    layers, stride, page_bytes = _kv_layers(cache, page_size, num_pages)
+    _same_device(refs, block_table=block_table, kv_lens=kv_lens, cache=cache, info=info, workspace=workspace)
+    with _on(refs):
+        if workspace is None:
+            workspace = torch.empty(kv_compact_workspace(num_pages), dtype=torch.uint8, device=refs.device)
+        _check(lib().mxq_kv_compact(_ptr(block_table), rows, cols, cols, _ptr(kv_lens), _ptr(refs), num_pages, page_size,
+                                    _ptr(cache), layers, stride, page_bytes, _ptr(info), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_compact")
+    return info
