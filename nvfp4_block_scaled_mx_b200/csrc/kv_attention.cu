@@ -19,6 +19,7 @@
 // CTA for itself from the lengths on the device, so that ragged batches balance and a graph can be
 // replayed with other lengths.  A CTA's part of a row tile that it does not have whole goes to the
 // workspace as (m, l, O); a second kernel joins those in CTA order, so results do not depend on timing.
+#include <algorithm>
 #include <atomic>
 
 #include "kv.cuh"
@@ -28,10 +29,24 @@
 namespace mxq {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMinTiles = 8;  // token tiles a CTA gets at least
+constexpr int kWarps = 4;                     // warps that compute; one more feeds them
+constexpr int kThreads = (kWarps + 1) * 32;
+#ifndef C_MINT
+#define C_MINT 4
+#endif
+constexpr int kMinTiles = C_MINT;  // token tiles a CTA gets at least
 constexpr float kNegMax = -3.402823466e38f;
+
+// A run of token tiles of one row tile and kv head, as the feeding warp describes it.
+struct Segment {
+    int count;                     // token tiles; -1: no more work
+    uint32_t base;                 // tiles in front of it in the CTA's ring
+    int pos0;                      // first token of its first tile
+    int seen0, seen1, all0, all1;  // tokens that any row sees, and that all rows see
+    int q0, row0, rows, head;      // first query row of the sequence, row tile, its rows, kv head
+    int begins, whole;             // has the row tile's first token tile; has all of them
+    int parts;                     // if it begins but is not whole: CTAs that have a part
+};
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -41,16 +56,25 @@ struct Cfg {
     static constexpr int ROWS = 8 * NT;
     static constexpr int KS = D / 16;  // k steps of S, m tiles of O
     static constexpr int TILE_BYTES = TU * U::BYTES;
-    static constexpr int STAGES = 3;
-    static constexpr int RING = kWarps * STAGES * TILE_BYTES;
     static constexpr int OSTRIDE = D + 8;  // floats; row pairs of a warp's float2 stores meet different banks
+    static constexpr int Q_BYTES = NT * KS * 32 * 8;
     static constexpr int RED = kWarps * ROWS * OSTRIDE * 4;
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = NT * KS * 32 * 8;
-    static constexpr int OFF_ROW = OFF_RING + (RING > RED ? RING : RED);  // per row: scale, first, end
-    static constexpr int OFF_ML = OFF_ROW + ROWS * 12;
-    static constexpr int OFF_BAR = (OFF_ML + kWarps * ROWS * 8 + 15) / 16 * 16;
-    static constexpr int BYTES = OFF_BAR + kWarps * STAGES * 8 + 64;
+    // CTAs an SM holds, by registers (an accumulator of 4 NT KS a lane), and what is left of its shared memory
+    static constexpr int CTAS = NT * KS <= 8 ? 3 : NT * KS <= 16 ? 2 : 1;
+    static constexpr int BUDGET = (227 / CTAS - 1) * 1024 - 1024;
+    static constexpr int FIXED = 2 * Q_BYTES + RED + 2 * (ROWS * 12 + 64) + kWarps * ROWS * 8 + 64;
+    static constexpr int FIT = (BUDGET - FIXED) / (TILE_BYTES + 16);
+    static constexpr int STAGES = FIT < 16 ? FIT : 16;
+    static_assert(STAGES >= kWarps, "shared memory");
+    static constexpr int OFF_RING = 0;
+    static constexpr int OFF_Q = STAGES * TILE_BYTES;
+    static constexpr int OFF_RED = OFF_Q + 2 * Q_BYTES;
+    static constexpr int OFF_ROW = OFF_RED + RED;  // two buffers; per row: scale, first, end
+    static constexpr int OFF_SEG = OFF_ROW + 2 * ROWS * 12;
+    static constexpr int OFF_ML = OFF_SEG + 2 * 64;
+    static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;  // full, empty, segment full, segment empty
+    static constexpr int BYTES = OFF_BAR + (2 * STAGES + 4) * 8;
+    static_assert(sizeof(Segment) <= 64, "segment note");
     static constexpr float SHIFT = FMT == MXQ_NVFP4 ? 7.0f : 4.0f;  // log2 of what P is multiplied by
 };
 
@@ -84,7 +108,7 @@ __device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b) {
 
 // Tokens [first, end) that row r of the sequence sees.
 __device__ __forceinline__ void row_span(const KvAttnArgs& a, const Seq& s, int r, int& first, int& end) {
-    const int seen = s.kv - s.qn + r / a.group + 1;
+    const int seen = s.kv - s.qn + (a.max_q == 1 ? 0 : r / a.group) + 1;
     end = a.causal ? max(seen, 0) : s.kv;
     first = a.window > 0 ? max(seen - a.window, 0) : 0;
 }
@@ -104,6 +128,7 @@ template <int TILE, int ROWS>
 __device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
     int64_t n = 0;
     const int tiles = (s.qn * a.group + ROWS - 1) / ROWS;
+#pragma unroll 1
     for (int qt = 0; qt < tiles; ++qt) {
         int t0;
         n += tile_span<TILE, ROWS>(a, s, qt, t0);
@@ -111,60 +136,95 @@ __device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
     return n * a.kv_heads;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// q = n / d, r = n % d; in 32 bits where the operands allow it.
+__device__ __forceinline__ int64_t div_mod(int64_t n, int64_t d, int64_t& r) {
+    int64_t q;
+    if (((n | d) >> 32) == 0) {
+        q = static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    } else {
+        q = n / d;
+    }
+    r = n - q * d;
+    return q;
 }
 
-// All work of the batch, in token tiles (whole warp).
-template <int TILE, int ROWS>
-__device__ __forceinline__ int64_t total_work(const KvAttnArgs& a) {
-    int64_t n = 0;
-    for (int b = threadIdx.x & 31; b < a.batch; b += 32) n += seq_cost<TILE, ROWS>(a, load_seq(a, b));
-    return warp_sum64(n);
-}
+// The cut of the batch's work, in token tiles: CTA c takes [c per, (c + 1) per).  Whole warp, every warp
+// for itself; `at` is this CTA's first tile, b and off the sequence that holds it and its place there.
+struct Plan {
+    int64_t work, per, at, off;
+    int b;
+};
 
-// The sequence that holds work item `at`, and the work in front of it (whole warp; at < total).
 template <int TILE, int ROWS>
-__device__ __forceinline__ int find_seq(const KvAttnArgs& a, int64_t at, int64_t& before) {
+__device__ __forceinline__ Plan make_plan(const KvAttnArgs& a) {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
+    Plan p;
+    int64_t own = 0, sum = 0;  // of the last 32 sequences: the lane's, and the inclusive scan over the lanes
+    p.work = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int64_t cost = b < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b)) : 0;
-        int64_t sum = cost;
+        own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
+        sum = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += x;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + sum > at);
+        p.work += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    int64_t rest;
+    p.per = div_mod(p.work + gridDim.x - 1, gridDim.x, rest);
+    if (p.per < kMinTiles) p.per = kMinTiles;
+    p.at = p.per * blockIdx.x;
+    p.b = a.batch;
+    p.off = 0;
+    if (p.at >= p.work) return p;
+    int64_t base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        if (a.batch > 32) {
+            own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
+            sum = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, base + sum > p.at);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            before = base + __shfl_sync(0xffffffffu, sum - cost, l);
-            return b0 + l;
+            p.off = p.at - base - __shfl_sync(0xffffffffu, sum - own, l);
+            p.b = b0 + l;
+            break;
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    before = base;
-    return a.batch;
+    return p;
 }
 
-__device__ __forceinline__ int64_t work_ctas(int64_t work, int grid) {
-    const int64_t n = (work + kMinTiles - 1) / kMinTiles;
-    return n < grid ? (n > 0 ? n : 1) : grid;
-}
+// What the join kernel needs to know of a row tile whose first part CTA c has; parts = 0: there is none.
+struct Split {
+    int parts, q0, row0, rows, head, pad[3];
+};
 
 // ------------------------------------------------------------------------------ instructions
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // 8 E2M1 codes as 4 f16x2: byte i of w becomes o[i], its low nibble in the low half.
@@ -239,7 +299,7 @@ template <int FMT, int D, int NT>
 struct Warp {
     using C = Cfg<FMT, D, NT>;
     float o[NT][C::KS][4];
-    float m[NT][2], l[NT][2];
+    float base[NT][2], l[NT][2];  // probabilities are 2^(s - base): base is the running maximum - SHIFT
     int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];  // MXFP4: E8M0 code that stands for 2^9 in the factors, per 32 channels
 };
 
@@ -252,7 +312,7 @@ __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
         for (int j = 0; j < C::KS; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w.o[n][j][i] = 0.0f;
-        w.m[n][0] = w.m[n][1] = kNegMax;
+        w.base[n][0] = w.base[n][1] = kNegMax;
         w.l[n][0] = w.l[n][1] = 0.0f;
     }
     if constexpr (FMT == MXQ_MXFP4) {
@@ -346,8 +406,8 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
                     const float f0 = __uint_as_float(sc[u][0][word]), f1 = __uint_as_float(sc[u][1][word]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_f16(c, lo[0], hi[0], lo[1], hi[1], q[n][0], q[n][1]);
+                        float c[4];
+                        mma_f16_first(c, lo[0], hi[0], lo[1], hi[1], q[n][0], q[n][1]);
                         mma_f16(c, lo[2], hi[2], lo[3], hi[3], q[n][2], q[n][3]);
                         s[u][n][0] = fmaf(c[0], f0, s[u][n][0]);
                         s[u][n][1] = fmaf(c[1], f0, s[u][n][1]);
@@ -376,43 +436,46 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
     float s[C::TU][NT][4];
     scores<FMT, D, NT>(tile, qf, s);
 
-    bool raise = false;
-    float top[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            int first = 0, end = 0;
-            if constexpr (MASK) first = row_first[8 * n + 2 * t + c], end = row_end[8 * n + 2 * t + c];
-            float x = kNegMax;
-#pragma unroll
-            for (int u = 0; u < C::TU; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v = s[u][n][2 * h + c] * cs[n][c];
-                    if constexpr (MASK) {
-                        const int pos = pos0 + 16 * u + 8 * h + g;
-                        if (pos < first || pos >= end) v = __int_as_float(0xff800000);
-                    }
-                    s[u][n][2 * h + c] = v;
-                    x = fmaxf(x, v);
-                }
-            top[n][c] = x;
-            raise = raise || x > w.m[n][c];
+    // exponents s cs - base; one above SHIFT (all of them, before the first tile) raises the row's base
+    auto exponent = [&](int u, int n, int i, float base) {
+        float v = fmaf(s[u][n][i], cs[n][i & 1], -base);
+        if constexpr (MASK) {
+            const int pos = pos0 + 16 * u + 8 * (i >> 1) + g, r = 8 * n + 2 * t + (i & 1);
+            if (pos < row_first[r] || pos >= row_end[r]) v = __int_as_float(0xff800000);
         }
-    if (__any_sync(0xffffffffu, raise)) {
+        return v;
+    };
+    float x[C::TU][NT][4];
+    float top = kNegMax;
+#pragma unroll
+    for (int u = 0; u < C::TU; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[u][n][i] = exponent(u, n, i, w.base[n][i & 1]);
+                top = fmaxf(top, x[u][n][i]);
+            }
+    if (__any_sync(0xffffffffu, top > C::SHIFT)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float al[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float x = top[n][c];
+                float m = kNegMax;
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                x = fmaxf(x, w.m[n][c]);
-                al[c] = ex2(w.m[n][c] - x);
-                w.m[n][c] = x;
+                for (int u = 0; u < C::TU; ++u) m = fmaxf(m, fmaxf(exponent(u, n, c, 0.0f), exponent(u, n, 2 + c, 0.0f)));
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float base = fmaxf(w.base[n][c], m - C::SHIFT);
+                al[c] = ex2(w.base[n][c] - base);
+                w.base[n][c] = base;
                 w.l[n][c] *= al[c];
+#pragma unroll
+                for (int u = 0; u < C::TU; ++u) {
+                    x[u][n][c] = exponent(u, n, c, base);
+                    x[u][n][2 + c] = exponent(u, n, 2 + c, base);
+                }
             }
 #pragma unroll
             for (int j = 0; j < C::KS; ++j) {
@@ -430,7 +493,7 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
         for (int n = 0; n < NT; ++n) {
             float e[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = ex2(s[u][n][i] - (w.m[n][i & 1] - C::SHIFT));
+            for (int i = 0; i < 4; ++i) e[i] = ex2(x[u][n][i]);
             w.l[n][0] += e[0] + e[2];
             w.l[n][1] += e[1] + e[3];
             p[n][0] = transpose8x8(cvt_f16x2(e[0], e[1]));
@@ -449,47 +512,50 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
             }
         }
         const uint32_t unit = tile + u * U::BYTES;
-        // scale factors of the pair's two tokens, f16x2 per scale block
-        uint32_t fac[2][U::NB];
+        // scale bytes of the pairs' tokens, then their factors, f16x2 per scale block
+        constexpr int PB = 2 * U::NB;  // bytes of a token pair's scales
+        uint32_t sb[2][PB / 4], fac[2][U::NB];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            constexpr int PB = 2 * U::NB;  // bytes of a token pair's scales
-            uint32_t x[PB / 4];
             const uint32_t at = unit + U::OFF_VS + (t + 4 * h) * PB;
             if constexpr (PB <= 16) {
-                lds<PB>(at, x);
+                lds<PB>(at, sb[h]);
             } else {
                 uint32_t y[4];
 #pragma unroll
                 for (int i = 0; i < PB / 16; ++i) {
                     lds<16>(at + 16 * i, y);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[4 * i + k] = y[k];
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < U::NB; ++b) {
-                const uint32_t pair = b & 1 ? x[b >> 1] >> 16 : x[b >> 1] & 0xFFFFu;
-                if constexpr (FMT == MXQ_NVFP4) {
-                    fac[h][b] = e4m3x2_f16x2(pair);
-                } else {
-                    fac[h][b] = prmt(pair, 0u, 0x4140u);  // the codes, one a half
-                    if constexpr (MASK) fac[h][b] &= live[h];
+                    for (int k = 0; k < 4; ++k) sb[h][4 * i + k] = y[k];
                 }
             }
         }
-        if constexpr (FMT == MXQ_MXFP4) {
-            // factors 2^(code - ref + 9) as f16 bits; a code more than 2 above ref moves ref (and O) up
-            bool over = false;
+        if constexpr (FMT == MXQ_NVFP4) {
 #pragma unroll
-            for (int b = 0; b < U::NB; ++b) {
-                const uint32_t hi = __vmaxu2(fac[0][b], fac[1][b]);
-                over = over || static_cast<int>(max(hi & 0xFFFFu, hi >> 16)) > w.ref[b] + 2;
-            }
-            if (__any_sync(0xffffffffu, over)) {
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int b = 0; b < U::NB; ++b) fac[h][b] = e4m3x2_f16x2(b & 1 ? sb[h][b >> 1] >> 16 : sb[h][b >> 1] & 0xFFFFu);
+        } else {
+            // 2^(code - ref + 9): the exponent fields code - ref + 24 of both halves, 0 where that is below 1
+            auto codes = [&](int h, int b) {  // one a half
+                const uint32_t x = prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);
+                return MASK ? x & live[h] : x;
+            };
+            auto fields = [&]() {
+                uint32_t most = 0;
 #pragma unroll
                 for (int b = 0; b < U::NB; ++b) {
-                    const uint32_t hi = __vmaxu2(fac[0][b], fac[1][b]);
+                    const uint32_t bias = static_cast<uint32_t>((24 - w.ref[b]) & 0xFFFF) * 0x10001u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) fac[h][b] = __viaddmax_s16x2_relu(codes(h, b), bias, 0u);
+                    most = __vimax3_u16x2(most, fac[0][b], fac[1][b]);
+                }
+                return max(most & 0xFFFFu, most >> 16);
+            };
+            if (__any_sync(0xffffffffu, fields() > 26u)) {  // a code more than 2 above ref moves ref (and O) up
+#pragma unroll
+                for (int b = 0; b < U::NB; ++b) {
+                    const uint32_t hi = __vmaxu2(codes(0, b), codes(1, b));
                     int code = static_cast<int>(max(hi & 0xFFFFu, hi >> 16));
                     code = max(code, __shfl_xor_sync(0xffffffffu, code, 1));
                     code = max(code, __shfl_xor_sync(0xffffffffu, code, 2));
@@ -504,13 +570,10 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
                                 for (int i = 0; i < 4; ++i) w.o[n][j][i] *= f;
                     }
                 }
+                fields();
             }
 #pragma unroll
-            for (int b = 0; b < U::NB; ++b) {
-                const uint32_t bias = static_cast<uint32_t>((24 - w.ref[b]) & 0xFFFF) * 0x10001u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) fac[h][b] = __viaddmax_s16x2_relu(fac[h][b], bias, 0u) << 10;
-            }
+            for (int b = 0; b < U::NB; ++b) fac[0][b] <<= 10, fac[1][b] <<= 10;
         }
         // V codes: this lane's D / 16 bytes of both tokens of either pair
         uint32_t v[2][2][D / 64];
@@ -553,54 +616,55 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
 
 // ------------------------------------------------------------------------------------- kernel
 
-// Writes one row's share: `x` two neighbouring channels.
-__device__ __forceinline__ void put2(const KvAttnArgs& a, int64_t at, float x, float y) {
+// Writes four neighbouring channels of a row.
+__device__ __forceinline__ void put4(const KvAttnArgs& a, int64_t at, float x, float y, float z, float w) {
     if (a.out_f32) {
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x, y);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(x, y, z, w);
     } else {
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) = __floats2bfloat162_rn(x, y);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x, y), hi = __floats2bfloat162_rn(z, w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
 }
 
+// The feeding warp: walks the CTA's work, notes each segment and its Q operands (two buffers), and keeps
+// the ring of token tiles full, so that the computing warps never wait for an index or a query.
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv_attention_kernel(const KvAttnArgs a) {
+__device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     using C = Cfg<FMT, D, NT>;
     using U = typename C::U;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    float* row_scale = reinterpret_cast<float*>(smem + C::OFF_ROW);
-    int* row_first = reinterpret_cast<int*>(row_scale + C::ROWS);
-    int* row_end = row_first + C::ROWS;
-    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
-    uint64_t* full = bars + warp * C::STAGES;
-    uint8_t* ring = smem + C::OFF_RING + warp * C::STAGES * C::TILE_BYTES;
-    const uint32_t qf = smem_u32(smem + C::OFF_Q);
+    const int lane = threadIdx.x & 31;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* seg_full = empty + C::STAGES;
+    uint64_t* seg_empty = seg_full + 2;
 
-    if (lane == 0) {
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1);
-        fence_barrier_init();
-    }
-    __syncthreads();
-    pdl_launch_dependents();
-    pdl_wait();
+    const Plan plan = make_plan<C::TILE, C::ROWS>(a);
+    if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
+    int64_t at = plan.at, off = plan.off;
+    const int64_t stop = min(at + plan.per, plan.work);
+    int b = plan.b, qt = 0;
+    Seq s = {};
+    if (at < stop) s = load_seq(a, b);
+    float qscale = a.scale * 1.4426950408889634f;
+    if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k;
+    uint32_t tiles = 0, nseg = 0;
 
-    // this CTA's part of the work (every warp for itself: the loads hit the same lines)
-    const int64_t work = total_work<C::TILE, C::ROWS>(a);
-    const int64_t ctas = work_ctas(work, gridDim.x);
-    if (blockIdx.x >= ctas || work == 0) return;
-    int64_t at = work * blockIdx.x / ctas;
-    const int64_t stop = work * (blockIdx.x + 1) / ctas;
-    int64_t before;
-    int b = find_seq<C::TILE, C::ROWS>(a, at, before);
-    int64_t off = at - before;  // work of the sequence in front of `at`
-    Seq s = load_seq(a, b);
-    int qt = 0;
-    uint32_t used = 0;  // tiles this warp has taken through its ring
-
-    while (at < stop) {
+#pragma unroll 1
+    for (;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        Segment* note = reinterpret_cast<Segment*>(smem + C::OFF_SEG + buf * 64);
+        if (at >= stop) {
+            if (!mbar_wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
+            if (lane == 0) {
+                note->count = -1;
+                mbar_arrive(&seg_full[buf]);
+            }
+            return;
+        }
         // the row tile and kv head that hold work item `at`
         int t0, n;
+#pragma unroll 1
         for (;;) {
             if (qt * C::ROWS >= s.qn * a.group) {
                 s = load_seq(a, ++b);
@@ -612,116 +676,193 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const KvAttnArgs
             off -= static_cast<int64_t>(n) * a.kv_heads;
             ++qt;
         }
-        const int head = static_cast<int>(off / n), from = static_cast<int>(off % n);
+        int64_t from64;
+        const int head = static_cast<int>(div_mod(off, n, from64)), from = static_cast<int>(from64);
         const int count = static_cast<int>(min(static_cast<int64_t>(n - from), stop - at));
-        const int rows = min(C::ROWS, s.qn * a.group - qt * C::ROWS);
-        const bool whole = from == 0 && count == n;
-        int seen0, seen1, skip;
-        row_span(a, s, qt * C::ROWS, seen0, skip);
-        row_span(a, s, qt * C::ROWS + rows - 1, skip, seen1);
-        // tokens that all rows see
-        int all0, all1;
-        row_span(a, s, qt * C::ROWS, skip, all1);
-        row_span(a, s, qt * C::ROWS + rows - 1, all0, skip);
+        const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.qn * a.group - row0);
+        int seen0, seen1, all0, all1;
+        row_span(a, s, row0, seen0, all1);
+        row_span(a, s, row0 + rows - 1, all0, seen1);
 
-        // this warp's tiles: from + warp, + kWarps, ...; lane i holds the page of the i-th unit ahead
-        const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
-        const int first_tile = t0 + from + warp;
-        const int units_end = (seen1 + 15) >> 4;  // units behind it are not loaded (their pages may not exist)
-        constexpr int AHEAD = 32 / C::TU;         // tiles whose pages one register per lane holds
-        auto page_of = [&](int batch) {
-            const int i = batch * AHEAD + lane / C::TU;
-            const int unit = (first_tile + i * kWarps) * C::TU + lane % C::TU;
-            if (i >= mine || unit >= units_end) return -1;
-            const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + unit / a.page_units];
+        // lane i holds the place of the i-th unit ahead: byte offset, -1 for one that is not loaded
+        const int first_unit = (t0 + from) * C::TU, end_unit = first_unit + count * C::TU;
+        const int units_end = min((seen1 + 15) >> 4, end_unit);  // behind the tokens pages may not exist
+        auto source_of = [&](int i) -> int64_t {
+            const int unit = first_unit + i + lane;
+            if (unit >= units_end) return -1;
+            const int at_page = unit / a.page_units;
+            const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             if (pg < 0 || pg >= a.num_pages) {
                 kv_status(a.status, kStatusKvPage);
                 return -1;
             }
-            return pg;
+            return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
+                   static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
         };
-        int pages = page_of(0), pages_next = page_of(1);
+        int64_t source = source_of(0), source_next = source_of(32);
         int issued = 0;
-        auto issue = [&]() {  // whole warp: start the copy of tile number `issued`
-            if (issued >= mine) return;
-            if (issued && issued % AHEAD == 0) {
-                pages = pages_next;
-                pages_next = page_of(issued / AHEAD + 1);
-            }
-            const uint32_t stage = (used + issued) % C::STAGES;
-            uint8_t* dst = ring + stage * C::TILE_BYTES;
-            uint32_t bytes = 0;
-            int64_t src[C::TU];
+        bool alive = true;
+        auto issue_until = [&](int limit, bool wait) {
+#pragma unroll 1
+            for (; issued < limit; ++issued, ++tiles) {
+                const int i = issued * C::TU % 32;
+                if (i == 0 && issued) {
+                    source = source_next;
+                    source_next = source_of(issued * C::TU + 32);
+                }
+                const uint32_t slot = tiles % C::STAGES;
+                if (wait && !mbar_wait_warp(&empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x42)) {
+                    alive = false;
+                    return;
+                }
+                int64_t src[C::TU];
 #pragma unroll
-            for (int u = 0; u < C::TU; ++u) {
-                const int pg = __shfl_sync(0xffffffffu, pages, (issued % AHEAD) * C::TU + u);
-                const int unit = (first_tile + issued * kWarps) * C::TU + u;
-                src[u] = pg < 0 ? -1
-                                : (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
-                                      static_cast<int64_t>(unit % a.page_units) * U::BYTES;
-                bytes += pg < 0 ? 0 : U::BYTES;
-            }
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&full[stage], bytes);
+                for (int u = 0; u < C::TU; ++u) src[u] = __shfl_sync(0xffffffffu, source, i + u);
+                if (elect_one()) {
+                    uint8_t* dst = smem + C::OFF_RING + slot * C::TILE_BYTES;
+                    uint32_t bytes = 0;
 #pragma unroll
-                for (int u = 0; u < C::TU; ++u)
-                    if (src[u] >= 0) bulk_load(dst + u * U::BYTES, a.cache + src[u], U::BYTES, &full[stage]);
+                    for (int u = 0; u < C::TU; ++u) bytes += src[u] < 0 ? 0 : U::BYTES;
+                    mbar_arrive_expect_tx(&full[slot], bytes);
+                    if (C::TU == 2 && src[0] >= 0 && src[C::TU - 1] == src[0] + U::BYTES) {  // neighbours in one page
+                        bulk_load(dst, a.cache + src[0], 2 * U::BYTES, &full[slot]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < C::TU; ++u)
+                            if (src[u] >= 0) bulk_load(dst + u * U::BYTES, a.cache + src[u], U::BYTES, &full[slot]);
+                    }
+                }
+                __syncwarp();
             }
-            ++issued;
         };
-#pragma unroll
-        for (int i = 0; i < C::STAGES; ++i) issue();
+        if (!mbar_wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
+        if (lane == 0) {
+            note->count = count;
+            note->base = tiles;
+            note->pos0 = (t0 + from) * C::TILE;
+            note->seen0 = seen0, note->seen1 = seen1, note->all0 = all0, note->all1 = all1;
+            note->q0 = s.q0, note->row0 = row0, note->rows = rows, note->head = head;
+            note->begins = from == 0;
+            note->whole = from == 0 && count == n;
+            int64_t rest;
+            note->parts = from == 0 ? static_cast<int>(div_mod(at + n - 1, plan.per, rest)) - static_cast<int>(blockIdx.x) + 1 : 0;
+        }
+        if (nseg == 0) issue_until(min(count, C::STAGES), false);  // the ring is empty: loads first
 
         // Q operands: rows as f16 times a power of two
-        for (int r = warp; r < C::ROWS; r += kWarps) {
-            constexpr int E = D / 32;  // elements of a lane
-            uint32_t x[E / 2];
-            float big = 0.0f;
+        float* row_scale = reinterpret_cast<float*>(smem + C::OFF_ROW + buf * C::ROWS * 12);
+        int* row_first = reinterpret_cast<int*>(row_scale + C::ROWS);
+        int* row_end = row_first + C::ROWS;
+        constexpr int E = D / 32;  // elements of a lane
+#pragma unroll 1
+        for (int r8 = 0; r8 < C::ROWS; r8 += 8) {
+            uint32_t x[8][E / 2];
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) x[i] = 0;
-            if (r < rows) {
-                const int row = qt * C::ROWS + r;
-                const __nv_bfloat16* src = a.q + static_cast<int64_t>(s.q0 + row / a.group) * a.q_token_stride +
-                                           static_cast<int64_t>(head * a.group + row % a.group) * a.q_head_stride + lane * E;
+            for (int k = 0; k < 8; ++k) {
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) x[i] = reinterpret_cast<const uint32_t*>(src)[i];
+                for (int i = 0; i < E / 2; ++i) x[k][i] = 0;
+                if (r8 + k < rows) {
+                    const int row = row0 + r8 + k, j = a.max_q == 1 ? 0 : row / a.group;
+                    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                        a.q + static_cast<int64_t>(s.q0 + j) * a.q_token_stride +
+                        static_cast<int64_t>(head * a.group + row - j * a.group) * a.q_head_stride + lane * E);
+                    if constexpr (E == 2) {
+                        x[k][0] = *src;
+                    } else if constexpr (E == 4) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(src);
+                        x[k][0] = y.x, x[k][1] = y.y;
+                    } else {
+                        const uint4 y = *reinterpret_cast<const uint4*>(src);
+                        x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                    }
+                }
             }
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i)
-                big = fmaxf(big, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const uint32_t ex = max(__float_as_uint(big) >> 23, 8u);
-            const float mul = __uint_as_float((261u - ex) << 23);
-            uint32_t h[E / 2];
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i)
-                h[i] = cvt_f16x2(__uint_as_float(x[i] << 16) * mul, __uint_as_float(x[i] & 0xFFFF0000u) * mul);
-            // element e of the row: lane (r % 8, qq) and k step st, as its A operand's codes are dealt
+            // element e of a row: lane (r % 8, qq) and k step st, as the K codes are dealt to the A operand
             const int e = lane * E;
-            int qq, st;
-            if constexpr (FMT == MXQ_NVFP4) {
-                qq = e / (D / 4);
-                st = e % (D / 4) / 4;
-            } else {
-                qq = e % 32 / 8;
-                st = 2 * (e / 32) + e % 8 / 4;
-            }
-            uint32_t* dst = reinterpret_cast<uint32_t*>(
-                smem + C::OFF_Q + (((r / 8) * (C::KS / 2) + st / 2) * 32 + (r % 8) * 4 + qq) * 16 + (st & 1) * 8 + e % 4 / 2 * 4);
+            const int qq = FMT == MXQ_NVFP4 ? e / (D / 4) : e % 32 / 8;
+            const int st = FMT == MXQ_NVFP4 ? e % (D / 4) / 4 : 2 * (e / 32) + e % 8 / 4;
+            uint8_t* dst = smem + C::OFF_Q + buf * C::Q_BYTES + ((r8 / 8) * (C::KS / 2) + st / 2) * 512 + qq * 16 + (st & 1) * 8 +
+                           e % 4 / 2 * 4;
+            uint32_t mine = 0;  // the exponent of the row that this lane notes
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) dst[i] = h[i];
-            if (lane == 0) {
-                float f = a.scale * 1.4426950408889634f;
-                if constexpr (FMT == MXQ_NVFP4) f *= *a.g_k;
-                row_scale[r] = f * __uint_as_float((ex - 7u) << 23);
+            for (int k = 0; k < 8; ++k) {
+                uint32_t top = 0;  // bf16 magnitudes order like integers
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[k][i] & 0x7FFF7FFFu);
+                const uint32_t big = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+                const uint32_t ex = max(big >> 7, 8u);
+                if ((lane & 7) == k) mine = ex;
+                const float mul = __uint_as_float((261u - ex) << 23);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i)
+                    *reinterpret_cast<uint32_t*>(dst + k * 64 + i * 4) =
+                        cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
+            }
+            if (lane < 8) {
+                const int r = r8 + lane;
+                row_scale[r] = qscale * __uint_as_float((mine - 7u) << 23);
                 int f0 = 0, f1 = 0;
-                if (r < rows) row_span(a, s, qt * C::ROWS + r, f0, f1);
+                if (r < rows) row_span(a, s, row0 + r, f0, f1);
                 row_first[r] = f0;
                 row_end[r] = f1;
             }
         }
-        __syncthreads();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_full[buf]);
+        issue_until(count, true);
+        if (!alive) return;
+        at += count;
+        off += count;
+    }
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_kernel(const KvAttnArgs a) {
+    using C = Cfg<FMT, D, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* seg_full = empty + C::STAGES;
+    uint64_t* seg_empty = seg_full + 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], kWarps);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == kWarps) {
+        feed<FMT, D, NT>(a, smem);
+        return;
+    }
+
+    float* partials = a.partial + gridDim.x * (sizeof(Split) / 4);
+    float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    bool dead = false;
+#pragma unroll 1
+    for (uint32_t nseg = 0;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        dead = !mbar_wait_warp(&seg_full[buf], nseg >> 1 & 1u, a.status, 0x43);
+        // one decision for the computing warps; also: the last segment's O has been read
+        if (named_barrier_or(1, kWarps * 32, dead)) return;
+        const Segment& seg = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
+        const int count = seg.count;
+        if (count < 0) return;
+        const float* row_scale = reinterpret_cast<const float*>(smem + C::OFF_ROW + buf * C::ROWS * 12);
+        const int* row_first = reinterpret_cast<const int*>(row_scale + C::ROWS);
+        const int* row_end = row_first + C::ROWS;
+        const uint32_t qf = smem_u32(smem + C::OFF_Q + buf * C::Q_BYTES);
+        const int seen0 = seg.seen0, seen1 = seg.seen1, all0 = seg.all0, all1 = seg.all1;
+        const uint32_t base = seg.base;
         float cs[NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -730,52 +871,39 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const KvAttnArgs
 
         Warp<FMT, D, NT> w;
         warp_reset(w);
-        bool dead = false;
-        for (int i = 0; i < mine; ++i) {
-            const uint32_t slot = (used + i) % C::STAGES;
-            if (!mbar_wait_warp(&full[slot], (used + i) / C::STAGES & 1u, a.status, 0x40)) {
+        int pos0 = seg.pos0 + warp * C::TILE;
+#pragma unroll 1
+        for (int i = warp; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
+            const uint32_t slot = (base + i) % C::STAGES;
+            if (!mbar_wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
                 dead = true;
                 break;
             }
-            const uint32_t tile = smem_u32(ring + slot * C::TILE_BYTES);
-            const int pos0 = (first_tile + i * kWarps) * C::TILE;
+            const uint32_t tile = smem_u32(smem + C::OFF_RING + slot * C::TILE_BYTES);
             if (pos0 >= all0 && pos0 + C::TILE <= all1)
                 tile_step<FMT, D, NT, false>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1);
             else
                 tile_step<FMT, D, NT, true>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1);
             __syncwarp();
-            issue();
+            if (lane == 0) mbar_arrive(&empty[slot]);
         }
-        used += mine;
 
-        // join the warps: each brings its O to the common maximum, then sums
+        // join the warps: each leaves (base, l, O); the sums are taken by all together
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float x = w.l[i][c];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (g == 0) ml[warp * C::ROWS + 8 * i + 2 * t + c] = make_float2(w.m[i][c], x);
-            }
-        if (__syncthreads_or(dead)) return;
-        float* red = reinterpret_cast<float*>(smem + C::OFF_RING);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            float f[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float top = kNegMax;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k * C::ROWS + 8 * i + 2 * t + c].x);
-                f[c] = ex2(w.m[i][c] - top);
+                if (g == 0) ml[warp * C::ROWS + 8 * i + 2 * t + c] = make_float2(w.base[i][c], x);
             }
 #pragma unroll
             for (int j = 0; j < C::KS; ++j) {
                 float x[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    x[k] = w.o[i][j][k] * f[k & 1];
+                    x[k] = w.o[i][j][k];
                     if constexpr (FMT == MXQ_MXFP4) x[k] = scale_pow2(x[k], max(w.ref[j / 2], 0) - 136);
                 }
                 float* dst = red + (warp * C::ROWS + 8 * i + 2 * t) * C::OSTRIDE + 16 * j + 2 * g;
@@ -783,98 +911,158 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const KvAttnArgs
                 *reinterpret_cast<float2*>(dst + C::OSTRIDE) = make_float2(x[1], x[3]);
             }
         }
-        __syncthreads();
-        float* part = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (from == 0 ? 1 : 0)) * (C::ROWS * (D + 2));
-        for (int i = threadIdx.x; i < C::ROWS * (D / 2); i += kThreads) {
-            const int r = i / (D / 2), d = i % (D / 2) * 2;
-            float top = kNegMax, sum = 0.0f, x = 0.0f, y = 0.0f;
+        if (named_barrier_or(1, kWarps * 32, dead)) return;
+        const int q0 = seg.q0, row0 = seg.row0, rows = seg.rows, head = seg.head;
+        const bool whole = seg.whole, begins = seg.begins;
+        // parts: a CTA has at most one that begins its row tile (the second slot) and one that does not
+        float* part = partials + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * (C::ROWS * (D + 2));
+        if (begins && !whole && threadIdx.x == 0) {
+            Split* split = reinterpret_cast<Split*>(a.partial) + blockIdx.x;
+            split->parts = seg.parts;
+            split->q0 = q0;
+            split->row0 = row0;
+            split->rows = rows;
+            split->head = head;
+        }
+        float gv = 1.0f;
+        if (FMT == MXQ_NVFP4 && whole) gv = *a.g_v;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < C::ROWS * (D / 4); i += kWarps * 32) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            float top = kNegMax, sum = 0.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k * C::ROWS + r].x);
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 const float2 z = ml[k * C::ROWS + r];
-                sum += z.y * ex2(z.x - top);
-                const float2 v = *reinterpret_cast<const float2*>(red + (k * C::ROWS + r) * C::OSTRIDE + d);
-                x += v.x;
-                y += v.y;
+                const float f = ex2(z.x - top);
+                const float4 v = *reinterpret_cast<const float4*>(red + (k * C::ROWS + r) * C::OSTRIDE + d);
+                sum = fmaf(z.y, f, sum);
+                x.x = fmaf(v.x, f, x.x);
+                x.y = fmaf(v.y, f, x.y);
+                x.z = fmaf(v.z, f, x.z);
+                x.w = fmaf(v.w, f, x.w);
             }
             if (whole) {
                 if (r < rows) {
-                    const int row = qt * C::ROWS + r;
-                    const int64_t o = static_cast<int64_t>(s.q0 + row / a.group) * a.heads + head * a.group + row % a.group;
-                    float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-                    if constexpr (FMT == MXQ_NVFP4) inv *= *a.g_v;
-                    put2(a, o * D + d, x * inv, y * inv);
+                    const int row = row0 + r, j = a.max_q == 1 ? 0 : row / a.group;
+                    const int64_t o = static_cast<int64_t>(q0 + j) * a.heads + head * a.group + row - j * a.group;
+                    const float inv = gv * (sum > 0.0f ? 1.0f / sum : sum);  // sum is 0 (no token) or not a number
+                    put4(a, o * D + d, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
                     if (a.lse && d == 0)
-                        a.lse[o] = sum == 0.0f ? __int_as_float(0xff800000)
-                                               : (top + (log2f(sum) - C::SHIFT)) * 0.6931471805599453f;
+                        a.lse[o] = sum == 0.0f ? __int_as_float(0xff800000) : (top + log2f(sum)) * 0.6931471805599453f;
                 }
             } else {
-                *reinterpret_cast<float2*>(part + r * D + d) = make_float2(x, y);
+                *reinterpret_cast<float4*>(part + r * D + d) = x;
                 if (d == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + 2 * r) = make_float2(top, sum);
             }
         }
-        fence_proxy_async_smem();  // the ring, written above by plain stores, takes bulk copies again
-        __syncthreads();
-        at += count;
-        off += count;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[buf]);
     }
 }
 
-// Joins the parts of the row tiles that several CTAs worked on: block x stands for the cut between CTAs
-// x and x + 1 and acts if that is the first cut inside its row tile; y slices the channels.
-constexpr int kJoinSlice = 32;
+// Joins the parts of the row tiles that several CTAs worked on, in CTA order.  Every block gathers the
+// list of those from all CTAs' notes; its items are (row tile, slice of 16 channels).  Latency is all
+// there is to it: the parts of an item are split among PG groups of threads, each of which has the loads
+// of BATCH parts in flight, so that 56 parts (a batch of one on all SMs) take one round trip.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxGrid = 1024;
+
+// Adds (m2, l2, v2) to the running (m, l, v): sums relative to 2^m.
+__device__ __forceinline__ void join_add(float& m, float& l, float4& v, float m2, float l2, const float4& v2) {
+    const float top = fmaxf(m, m2), f = ex2(m - top), f2 = ex2(m2 - top);
+    m = top;
+    l = l * f + l2 * f2;
+    v.x = v.x * f + v2.x * f2;
+    v.y = v.y * f + v2.y * f2;
+    v.z = v.z * f + v2.z * f2;
+    v.w = v.w * f + v2.w * f2;
+}
+
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvAttnArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const KvAttnArgs a, int grid) {
     using C = Cfg<FMT, D, NT>;
+    constexpr int SLICE = 16, SLICES = D / SLICE, ELEMS = C::ROWS * SLICE / 4, PG = kJoinThreads / ELEMS, BATCH = 8;
+    __shared__ uint32_t has[kMaxGrid / 32];
+    __shared__ int list[kMaxGrid], count;
+    __shared__ float2 mls[PG][ELEMS];
+    __shared__ float4 vs[PG][ELEMS];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t work = total_work<C::TILE, C::ROWS>(a);
-    const int64_t ctas = work_ctas(work, grid);
-    const int64_t me = blockIdx.x;
-    if (me + 1 >= ctas || work == 0) return;
-    const int64_t cut = work * (me + 1) / ctas;
-    int64_t before;
-    const int b = find_seq<C::TILE, C::ROWS>(a, cut, before);
-    const Seq s = load_seq(a, b);
-    int64_t off = cut - before;
-    int qt = 0, n, t0;
-    for (;; ++qt) {
-        n = tile_span<C::TILE, C::ROWS>(a, s, qt, t0);
-        if (off < static_cast<int64_t>(n) * a.kv_heads) break;
-        off -= static_cast<int64_t>(n) * a.kv_heads;
+    const Split* splits = reinterpret_cast<const Split*>(a.partial);
+    const float* partials = a.partial + grid * (sizeof(Split) / 4);
+    const float gv = FMT == MXQ_NVFP4 ? *a.g_v : 1.0f;
+    // the list is the same in every block: CTAs in order, placed by counting those in front
+    uint32_t mask[kMaxGrid / kJoinThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
+        const int c = i * kJoinThreads + threadIdx.x;
+        mask[i] = c < grid ? splits[c].parts : 0;
     }
-    const int head = static_cast<int>(off / n), from = static_cast<int>(off % n);
-    if (from == 0) return;                        // the cut lies between two row tiles
-    const int64_t begin = cut - from, end = begin + n;
-    if (work * me / ctas > begin) return;         // an earlier cut lies in this row tile
-    int parts = 1;
-    while (work * (me + parts) / ctas < end) ++parts;  // CTAs me .. me + parts - 1 have a part
-    const int rows = min(C::ROWS, s.qn * a.group - qt * C::ROWS);
-    constexpr int64_t PART = C::ROWS * (D + 2);
-    auto part = [&](int k) { return a.partial + ((me + k) * 2 + (k == 0 ? 1 : 0)) * PART; };
-    for (int i = threadIdx.x; i < rows * (kJoinSlice / 2); i += 256) {
-        const int r = i / (kJoinSlice / 2), d = blockIdx.y * kJoinSlice + i % (kJoinSlice / 2) * 2;
-        float top = kNegMax;
-#pragma unroll 8
-        for (int k = 0; k < parts; ++k) top = fmaxf(top, part(k)[C::ROWS * D + 2 * r]);
-        float sum = 0.0f, x = 0.0f, y = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < parts; ++k) {
-            const float2 z = *reinterpret_cast<const float2*>(part(k) + C::ROWS * D + 2 * r);
-            const float2 v = *reinterpret_cast<const float2*>(part(k) + r * D + d);
-            const float f = ex2(z.x - top);
-            sum += z.y * f;
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
+#pragma unroll
+    for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, mask[i] != 0);
+        if ((threadIdx.x & 31) == 0) has[(i * kJoinThreads + threadIdx.x) / 32] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        static_assert(kMaxGrid == 32 * 32, "one word of the mask a lane");
+        uint32_t m = has[threadIdx.x];
+        int before = __popc(m);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, before, o);
+            if (static_cast<int>(threadIdx.x) >= o) before += x;
         }
-        const int row = qt * C::ROWS + r;
-        const int64_t o = static_cast<int64_t>(s.q0 + row / a.group) * a.heads + head * a.group + row % a.group;
-        float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-        if constexpr (FMT == MXQ_NVFP4) inv *= *a.g_v;
-        put2(a, o * D + d, x * inv, y * inv);
-        if (a.lse && d == 0)
-            a.lse[o] = sum == 0.0f ? __int_as_float(0xff800000) : (top + (log2f(sum) - C::SHIFT)) * 0.6931471805599453f;
+        if (threadIdx.x == 31) count = before;
+        before -= __popc(m);
+        for (; m; m &= m - 1) list[before++] = threadIdx.x * 32 + __ffs(m) - 1;
+    }
+    __syncthreads();
+    constexpr int PART = C::ROWS * (D + 2);
+    const int pg = threadIdx.x / ELEMS, e = threadIdx.x % ELEMS, r = e / (SLICE / 4);
+#pragma unroll 1
+    for (int i = blockIdx.x; i < count * SLICES; i += gridDim.x) {
+        const int c = list[i / SLICES], d = i % SLICES * SLICE + e % (SLICE / 4) * 4;
+        const Split s = splits[c];
+        // slot 1 of the first CTA, slot 0 of the others
+        const float* first = partials + (static_cast<int64_t>(c) * 2 + 1) * PART;
+        float m = kNegMax, l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int k0 = pg; k0 < s.parts; k0 += PG * BATCH) {
+            float2 z[BATCH];
+            float4 x[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int k = k0 + j * PG;
+                const float* at = first + (k == 0 ? 0 : (2 * k - 1) * static_cast<int64_t>(PART));
+                z[j] = make_float2(kNegMax, 0.0f);
+                x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k < s.parts) {
+                    z[j] = *reinterpret_cast<const float2*>(at + C::ROWS * D + 2 * r);
+                    x[j] = *reinterpret_cast<const float4*>(at + r * D + d);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) join_add(m, l, v, z[j].x, z[j].y, x[j]);
+        }
+        mls[pg][e] = make_float2(m, l);
+        vs[pg][e] = v;
+        __syncthreads();
+        if (pg == 0 && r < s.rows) {
+#pragma unroll
+            for (int k = 1; k < PG; ++k) join_add(m, l, v, mls[k][e].x, mls[k][e].y, vs[k][e]);
+            const int row = s.row0 + r;
+            const int64_t o = static_cast<int64_t>(s.q0 + row / a.group) * a.heads + s.head * a.group + row % a.group;
+            const float inv = gv * (l > 0.0f ? 1.0f / l : l);  // l is 0 (no token) or not a number
+            put4(a, o * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            if (a.lse && d == 0)
+                a.lse[o] = l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
+        }
+        __syncthreads();
     }
 }
 
@@ -906,7 +1094,7 @@ int run(const KvAttnArgs& a, cudaStream_t st) {
         if (per_sm > kMaxCtasPerSm) per_sm = kMaxCtasPerSm;
         known[dev].store(per_sm);
     }
-    const int grid = sm_count() * per_sm;
+    const int grid = std::min(sm_count() * per_sm, kMaxGrid);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -918,8 +1106,8 @@ int run(const KvAttnArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return MXQ_ERR_CUDA;
-    cfg.gridDim = dim3(grid - 1, D / kJoinSlice);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(2 * sm_count());
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join, a, grid) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
@@ -936,7 +1124,7 @@ int run_dim(int D, int nt, const KvAttnArgs& a, cudaStream_t st) {
 size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_heads, int D) {
     (void)batch;
     const int rows = 8 * n_tiles(max_q * (heads / kv_heads), D);
-    return static_cast<size_t>(sm_count()) * kMaxCtasPerSm * 2 * rows * (D + 2) * 4;
+    return static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * rows * (D + 2) * 4 + sizeof(Split));
 }
 
 int launch_kv_attention(int fmt, int D, KvAttnArgs& a, cudaStream_t st) {
