@@ -169,7 +169,7 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
     if (!cache_ok(num_pages, page_size, kv_heads, head_dim) || heads < 1 || heads > (1 << 20) || heads % kv_heads != 0 ||
         batch < 0 || batch >= (int64_t(1) << 24) || rows < 0 || rows >= kInt || max_q < 1 || max_q >= kInt ||
         max_q * (heads / kv_heads) >= (int64_t(1) << 28) || max_pages < 1 || table_stride < max_pages ||
-        table_stride >= (int64_t(1) << 40) || max_pages * page_size >= kInt - 1024 || window < 0 || window >= kInt ||
+        table_stride >= (int64_t(1) << 40) || max_pages * page_size > (int64_t(1) << 30) - 1024 || window < 0 || window >= kInt ||
         !stride_ok(q_token_stride) || !stride_ok(q_head_stride) || (!q_start && rows != batch * max_q))
         return MXQ_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(block_table, 4) ||
@@ -201,6 +201,7 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
     a.kv_heads = kv_heads;
     a.group = heads / kv_heads;
     a.page_units = page_size / 16;
+    a.page_magic = a.page_units == 1 ? 0 : static_cast<uint32_t>(((uint64_t(1) << 32) + a.page_units - 1) / a.page_units);
     a.num_pages = static_cast<int>(num_pages);
     a.max_len = static_cast<int>(max_pages * page_size);
     a.causal = causal != 0;

@@ -83,7 +83,7 @@ struct Seq {
     int kv, q0, qn;  // tokens in the cache, first query row, query rows
 };
 
-__device__ __forceinline__ Seq load_seq(const KvAttnArgs& a, int b) {
+__device__ __noinline__ Seq load_seq(const KvAttnArgs& a, int b) {
     Seq s;
     s.kv = a.lens[b];
     if (s.kv > a.max_len) {
@@ -136,15 +136,13 @@ __device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
     return n * a.kv_heads;
 }
 
-// q = n / d, r = n % d; in 32 bits where the operands allow it.
-__device__ __forceinline__ int64_t div_mod(int64_t n, int64_t d, int64_t& r) {
-    int64_t q;
-    if (((n | d) >> 32) == 0) {
-        q = static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
-    } else {
-        q = n / d;
-    }
+// n / d for quotients below 2^20: a float quotient, corrected by at most a step or two (a 64-bit division
+// is many more instructions, and this code runs once per segment from a cold instruction cache).
+__device__ __forceinline__ int div_small(int64_t n, int64_t d, int64_t& r) {
+    int q = static_cast<int>(__fdividef(static_cast<float>(n), static_cast<float>(d)));
     r = n - q * d;
+    while (r < 0) r += d, --q;
+    while (r >= d) r -= d, ++q;
     return q;
 }
 
@@ -172,8 +170,8 @@ __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a) {
         }
         p.work += __shfl_sync(0xffffffffu, sum, 31);
     }
-    int64_t rest;
-    p.per = div_mod(p.work + gridDim.x - 1, gridDim.x, rest);
+    // any share that covers the work will do: the quotient in floats, rounded up past its error of 2^-22
+    p.per = static_cast<int64_t>(static_cast<float>(p.work) * a.inv_grid * 1.000001f) + 1;
     if (p.per < kMinTiles) p.per = kMinTiles;
     p.at = p.per * blockIdx.x;
     p.b = a.batch;
@@ -291,6 +289,17 @@ __device__ __forceinline__ float scale_pow2(float x, int e) {
         e += 126;
     }
     return x * __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+}
+
+// mbar_wait_warp with the waiting loop out of line: there are many waits, and their code counts.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* status, int where) {
+    return mbar_wait(bar, parity, status, where);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status, int where) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, wait_slow(bar, parity, status, where));
+    else ok = true;
+    return ok;
 }
 
 // --------------------------------------------------------------------------------- warp state
@@ -420,13 +429,14 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
     }
 }
 
-// Masks of the f16 pair (tokens pos, pos + 1) for a row that sees [first, end).
+// Mask of the scale bytes of tokens pos (even bytes) and pos + 1 that lie in [first, end).
 __device__ __forceinline__ uint32_t pair_mask(int pos, int first, int end) {
-    return (pos >= first && pos < end ? 0x0000FFFFu : 0u) | (pos + 1 >= first && pos + 1 < end ? 0xFFFF0000u : 0u);
+    return (pos >= first && pos < end ? 0x00FF00FFu : 0u) | (pos + 1 >= first && pos + 1 < end ? 0xFF00FF00u : 0u);
 }
 
 // One token tile: scores, softmax update, O update.  pos0 is the tile's first token; MASK: some row does
-// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees.
+// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees.  (One copy of the code
+// with branches in it took 75 us where the two take 65: the branches part what the scheduler interleaves.)
 template <int FMT, int D, int NT, bool MASK>
 __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, uint32_t qf, const float (&cs)[NT][2],
                                           const int* row_first, const int* row_end, int pos0, int seen0, int seen1) {
@@ -499,18 +509,6 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
             p[n][0] = transpose8x8(cvt_f16x2(e[0], e[1]));
             p[n][1] = transpose8x8(cvt_f16x2(e[2], e[3]));
         }
-        uint32_t keep[NT][2];
-        uint32_t live[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // tokens any row sees
-        if constexpr (MASK) {
-            const int pos = pos0 + 16 * u + 2 * t;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                live[h] = pair_mask(pos + 8 * h, seen0, seen1);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    keep[n][h] = pair_mask(pos + 8 * h, row_first[8 * n + g], row_end[8 * n + g]);
-            }
-        }
         const uint32_t unit = tile + u * U::BYTES;
         // scale bytes of the pairs' tokens, then their factors, f16x2 per scale block
         constexpr int PB = 2 * U::NB;  // bytes of a token pair's scales
@@ -530,6 +528,20 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
                 }
             }
         }
+        if constexpr (MASK) {
+            // P is 0 where a row does not see a token, but 0 times what is no number would not be: the scales
+            // of tokens that no row sees become 0, and a NaN (the quantizer writes none) the largest number
+            const int pos = pos0 + 16 * u + 2 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t live = pair_mask(pos + 8 * h, seen0, seen1);
+#pragma unroll
+                for (int i = 0; i < PB / 4; ++i) {
+                    sb[h][i] &= live;
+                    if constexpr (FMT == MXQ_NVFP4) sb[h][i] = __vminu4(sb[h][i] & 0x7F7F7F7Fu, 0x7E7E7E7Eu);
+                }
+            }
+        }
         if constexpr (FMT == MXQ_NVFP4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -538,8 +550,7 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
         } else {
             // 2^(code - ref + 9): the exponent fields code - ref + 24 of both halves, 0 where that is below 1
             auto codes = [&](int h, int b) {  // one a half
-                const uint32_t x = prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);
-                return MASK ? x & live[h] : x;
+                return prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);
             };
             auto fields = [&]() {
                 uint32_t most = 0;
@@ -606,7 +617,6 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     uint32_t b0 = hmul2(p[n][0], fac[0][b]), b1 = hmul2(p[n][1], fac[1][b]);
-                    if constexpr (MASK) b0 &= keep[n][0], b1 &= keep[n][1];
                     mma_f16(w.o[n][j], a[0][i], a[1][i], a[2][i], a[3][i], b0, b1);
                 }
             }
@@ -655,7 +665,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
         const uint32_t buf = nseg & 1u;
         Segment* note = reinterpret_cast<Segment*>(smem + C::OFF_SEG + buf * 64);
         if (at >= stop) {
-            if (!mbar_wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
+            if (!wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
             if (lane == 0) {
                 note->count = -1;
                 mbar_arrive(&seg_full[buf]);
@@ -677,7 +687,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             ++qt;
         }
         int64_t from64;
-        const int head = static_cast<int>(div_mod(off, n, from64)), from = static_cast<int>(from64);
+        const int head = div_small(off, n, from64), from = static_cast<int>(from64);
         const int count = static_cast<int>(min(static_cast<int64_t>(n - from), stop - at));
         const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.qn * a.group - row0);
         int seen0, seen1, all0, all1;
@@ -690,7 +700,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
         auto source_of = [&](int i) -> int64_t {
             const int unit = first_unit + i + lane;
             if (unit >= units_end) return -1;
-            const int at_page = unit / a.page_units;
+            const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));  // unit / page_units
             const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             if (pg < 0 || pg >= a.num_pages) {
                 kv_status(a.status, kStatusKvPage);
@@ -699,22 +709,49 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
                    static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
         };
-        int64_t source = source_of(0), source_next = source_of(32);
-        int issued = 0;
-        bool alive = true;
-        auto issue_until = [&](int limit, bool wait) {
+        int64_t source = -1, source_next = source_of(0);
+        // Q rows in flight beside them: lane (g, t) takes what it needs of row g as the B operand of S, 8
+        // elements (two k steps) a load, as the K codes are dealt to the lanes
+        constexpr int LOADS = D / 32;
+        const int g = lane >> 2, t = lane & 3;
+        uint4 x[LOADS];
+        auto load_rows = [&](int r8) {
+            const int row = row0 + r8 + g, j = a.max_q == 1 ? 0 : row / a.group;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(s.q0 + j) * a.q_token_stride +
+                                                              static_cast<int64_t>(head * a.group + row - j * a.group) * a.q_head_stride);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (r8 + g < rows) x[i] = src[FMT == MXQ_NVFP4 ? t * LOADS + i : i * 4 + t];
+            }
+        };
+        load_rows(0);
+        if (!wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
+        if (lane == 0) {
+            note->count = count;
+            note->base = tiles;
+            note->pos0 = (t0 + from) * C::TILE;
+            note->seen0 = seen0, note->seen1 = seen1, note->all0 = all0, note->all1 = all1;
+            note->q0 = s.q0, note->row0 = row0, note->rows = rows, note->head = head;
+            note->begins = from == 0;
+            note->whole = from == 0 && count == n;
+            int64_t rest;
+            note->parts = from == 0 ? div_small(at + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
+        }
+        // The first segment's copies start in front of its note (the ring is empty); later ones behind it,
+        // as their slots come free only while the computing warps are at the segment before.
+        int issued = 0, limit = nseg == 0 ? min(count, C::STAGES) : 0;
+#pragma unroll 1
+        for (int phase = 0; phase < 2; ++phase, limit = count) {
 #pragma unroll 1
             for (; issued < limit; ++issued, ++tiles) {
                 const int i = issued * C::TU % 32;
-                if (i == 0 && issued) {
+                if (i == 0) {
                     source = source_next;
                     source_next = source_of(issued * C::TU + 32);
                 }
                 const uint32_t slot = tiles % C::STAGES;
-                if (wait && !mbar_wait_warp(&empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x42)) {
-                    alive = false;
-                    return;
-                }
+                if (!wait_warp(&empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x42)) return;
                 int64_t src[C::TU];
 #pragma unroll
                 for (int u = 0; u < C::TU; ++u) src[u] = __shfl_sync(0xffffffffu, source, i + u);
@@ -734,90 +771,53 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
                 }
                 __syncwarp();
             }
-        };
-        if (!mbar_wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
-        if (lane == 0) {
-            note->count = count;
-            note->base = tiles;
-            note->pos0 = (t0 + from) * C::TILE;
-            note->seen0 = seen0, note->seen1 = seen1, note->all0 = all0, note->all1 = all1;
-            note->q0 = s.q0, note->row0 = row0, note->rows = rows, note->head = head;
-            note->begins = from == 0;
-            note->whole = from == 0 && count == n;
-            int64_t rest;
-            note->parts = from == 0 ? static_cast<int>(div_mod(at + n - 1, plan.per, rest)) - static_cast<int>(blockIdx.x) + 1 : 0;
-        }
-        if (nseg == 0) issue_until(min(count, C::STAGES), false);  // the ring is empty: loads first
-
-        // Q operands: rows as f16 times a power of two
-        float* row_scale = reinterpret_cast<float*>(smem + C::OFF_ROW + buf * C::ROWS * 12);
-        int* row_first = reinterpret_cast<int*>(row_scale + C::ROWS);
-        int* row_end = row_first + C::ROWS;
-        constexpr int E = D / 32;  // elements of a lane
+            if (phase == 1) break;
+            // Q operands: rows as f16 times a power of two
+            float* row_scale = reinterpret_cast<float*>(smem + C::OFF_ROW + buf * C::ROWS * 12);
+            int* row_first = reinterpret_cast<int*>(row_scale + C::ROWS);
+            int* row_end = row_first + C::ROWS;
 #pragma unroll 1
-        for (int r8 = 0; r8 < C::ROWS; r8 += 8) {
-            uint32_t x[8][E / 2];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-#pragma unroll
-                for (int i = 0; i < E / 2; ++i) x[k][i] = 0;
-                if (r8 + k < rows) {
-                    const int row = row0 + r8 + k, j = a.max_q == 1 ? 0 : row / a.group;
-                    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                        a.q + static_cast<int64_t>(s.q0 + j) * a.q_token_stride +
-                        static_cast<int64_t>(head * a.group + row - j * a.group) * a.q_head_stride + lane * E);
-                    if constexpr (E == 2) {
-                        x[k][0] = *src;
-                    } else if constexpr (E == 4) {
-                        const uint2 y = *reinterpret_cast<const uint2*>(src);
-                        x[k][0] = y.x, x[k][1] = y.y;
-                    } else {
-                        const uint4 y = *reinterpret_cast<const uint4*>(src);
-                        x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-                    }
-                }
-            }
-            // element e of a row: lane (r % 8, qq) and k step st, as the K codes are dealt to the A operand
-            const int e = lane * E;
-            const int qq = FMT == MXQ_NVFP4 ? e / (D / 4) : e % 32 / 8;
-            const int st = FMT == MXQ_NVFP4 ? e % (D / 4) / 4 : 2 * (e / 32) + e % 8 / 4;
-            uint8_t* dst = smem + C::OFF_Q + buf * C::Q_BYTES + ((r8 / 8) * (C::KS / 2) + st / 2) * 512 + qq * 16 + (st & 1) * 8 +
-                           e % 4 / 2 * 4;
-            uint32_t mine = 0;  // the exponent of the row that this lane notes
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int r8 = 0; r8 < C::ROWS; r8 += 8) {
+                if (r8) load_rows(r8);
                 uint32_t top = 0;  // bf16 magnitudes order like integers
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[k][i] & 0x7FFF7FFFu);
-                const uint32_t big = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+                for (int i = 0; i < LOADS; ++i)
+                    top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu)),
+                                   __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+                uint32_t big = max(top & 0xFFFFu, top >> 16);
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 const uint32_t ex = max(big >> 7, 8u);
-                if ((lane & 7) == k) mine = ex;
                 const float mul = __uint_as_float((261u - ex) << 23);
+                uint8_t* dst = smem + C::OFF_Q + buf * C::Q_BYTES + (r8 / 8) * (C::KS / 2) * 512 + lane * 16;
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i)
-                    *reinterpret_cast<uint32_t*>(dst + k * 64 + i * 4) =
-                        cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
+                for (int i = 0; i < LOADS; ++i) {
+                    const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = cvt_f16x2(__uint_as_float(y[k] << 16) * mul, __uint_as_float(y[k] & 0xFFFF0000u) * mul);
+                    *reinterpret_cast<uint4*>(dst + i * 512) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                if (t == 0) {
+                    const int r = r8 + g;
+                    row_scale[r] = qscale * __uint_as_float((ex - 7u) << 23);
+                    int f0 = 0, f1 = 0;
+                    if (r < rows) row_span(a, s, row0 + r, f0, f1);
+                    row_first[r] = f0;
+                    row_end[r] = f1;
+                }
             }
-            if (lane < 8) {
-                const int r = r8 + lane;
-                row_scale[r] = qscale * __uint_as_float((mine - 7u) << 23);
-                int f0 = 0, f1 = 0;
-                if (r < rows) row_span(a, s, row0 + r, f0, f1);
-                row_first[r] = f0;
-                row_end[r] = f1;
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_full[buf]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_full[buf]);
-        issue_until(count, true);
-        if (!alive) return;
         at += count;
         off += count;
     }
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
     using C = Cfg<FMT, D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 #pragma unroll 1
     for (uint32_t nseg = 0;; ++nseg) {
         const uint32_t buf = nseg & 1u;
-        dead = !mbar_wait_warp(&seg_full[buf], nseg >> 1 & 1u, a.status, 0x43);
+        dead = !wait_warp(&seg_full[buf], nseg >> 1 & 1u, a.status, 0x43);
         // one decision for the computing warps; also: the last segment's O has been read
         if (named_barrier_or(1, kWarps * 32, dead)) return;
         const Segment& seg = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 #pragma unroll 1
         for (int i = warp; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
             const uint32_t slot = (base + i) % C::STAGES;
-            if (!mbar_wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
+            if (!wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
                 dead = true;
                 break;
             }
@@ -982,7 +982,7 @@ __device__ __forceinline__ void join_add(float& m, float& l, float4& v, float m2
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const KvAttnArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const __grid_constant__ KvAttnArgs a, int grid) {
     using C = Cfg<FMT, D, NT>;
     constexpr int SLICE = 16, SLICES = D / SLICE, ELEMS = C::ROWS * SLICE / 4, PG = kJoinThreads / ELEMS, BATCH = 8;
     __shared__ uint32_t has[kMaxGrid / 32];
@@ -1078,7 +1078,7 @@ int n_tiles(int64_t rows, int D) {
 constexpr int kMaxCtasPerSm = 4;
 
 template <int FMT, int D, int NT>
-int run(const KvAttnArgs& a, cudaStream_t st) {
+int run(KvAttnArgs& a, cudaStream_t st) {
     using C = Cfg<FMT, D, NT>;
     auto kernel = kv_attention_kernel<FMT, D, NT>;
     auto join = kv_attention_join_kernel<FMT, D, NT>;
@@ -1105,6 +1105,7 @@ int run(const KvAttnArgs& a, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    a.inv_grid = 1.0f / static_cast<float>(grid);
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return MXQ_ERR_CUDA;
     cfg.gridDim = dim3(2 * sm_count());
     cfg.blockDim = dim3(kJoinThreads);
@@ -1113,7 +1114,7 @@ int run(const KvAttnArgs& a, cudaStream_t st) {
 }
 
 template <int FMT>
-int run_dim(int D, int nt, const KvAttnArgs& a, cudaStream_t st) {
+int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
     if (D == 64) return nt == 1 ? run<FMT, 64, 1>(a, st) : nt == 2 ? run<FMT, 64, 2>(a, st) : run<FMT, 64, 4>(a, st);
     if (D == 128) return nt == 1 ? run<FMT, 128, 1>(a, st) : nt == 2 ? run<FMT, 128, 2>(a, st) : run<FMT, 128, 4>(a, st);
     return nt == 1 ? run<FMT, 256, 1>(a, st) : run<FMT, 256, 2>(a, st);

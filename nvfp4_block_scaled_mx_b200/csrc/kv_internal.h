@@ -43,9 +43,10 @@ struct KvAttnArgs {
     float* partial;
     int batch, rows_total, max_q, heads, kv_heads, group;
     int page_units;              // units of a page
+    uint32_t page_magic;         // unit / page_units = high half of unit * page_magic, for units below 2^26
     int num_pages, max_len;      // max_len = table columns * page_size
     int causal, window, out_f32;
-    float scale;
+    float scale, inv_grid;
     int* status;
 };
 
