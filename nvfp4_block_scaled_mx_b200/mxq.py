@@ -358,6 +358,14 @@ def linear(x, W_q, W_sf, N, fmt, act_rule=CEIL, out_dtype=torch.bfloat16, g_W=No
 
 
 # ---------------------------------------------------------------- 4-bit key/value cache
+#
+# These calls take a few microseconds on the device, so the checks in front of them are written to cost
+# little: plain attribute reads, no device context unless the tensors lie on another device than the
+# current one, and the current stream's handle straight from the runtime.
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_KV_UNIT = {(f, d): 16 * d + 32 * (d // b) for f, b in ((MXFP4, 32), (NVFP4, 16)) for d in (64, 128, 256)}
+
 
 def kv_unit_bytes(head_dim, fmt):
     """Bytes of a unit of the cache: 16 tokens of one head, keys and values."""
@@ -374,37 +382,53 @@ def kv_cache_shape(num_pages, kv_heads, head_dim, fmt, page_size, layers=None):
     return shape if layers is None else (layers,) + shape
 
 
-def _same_device(first, **others):
-    """All tensors of a call lie on one device; it need not be the current one (see _on)."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, first.device))
+def _call(name, device, stream, *args):
+    """The C call `name` on `device` (that of its tensors, whatever the current one is), on `stream` or the
+    device's current stream."""
+    fn = getattr(lib(), name)
+    if device.type != "cuda":
+        if stream is None:
+            stream = _stream()
+        rc = fn(*args, stream)
+    elif device.index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MxqError(rc, name)
 
 
 def _on(t):
-    """The call's launches go to the device of its tensors, on that device's current stream by default."""
+    """The device context of a tensor's device, where a size depends on the device."""
     return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
 
 
-def _need_ints(t, name, n=None):
+def _at(t, name, dtype, n, device):
+    """Pointer of a contiguous tensor of at least n elements of dtype on the call's device (None passes)."""
     if t is None:
-        return
-    if t.dtype != torch.int32:
-        raise MxqBufferError("%s must be torch.int32 (got %s)" % (name, t.dtype))
-    if n is not None and t.numel() < n:
+        return None
+    if t.dtype is not dtype:
+        raise MxqBufferError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if t.numel() < n:
         raise MxqBufferError("%s holds %d values, the call needs %d" % (name, t.numel(), n))
+    if t.device != device:
+        raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
+    return _ptr(t)
 
 
-def _strided(t, name, heads=None, dim=None):
-    """[tokens, heads, dim] bf16 whose last dimension is contiguous: (token stride, head stride) in elements."""
-    if t.dtype != torch.bfloat16:
+def _rows(t, name, device):
+    """[tokens, heads, dim] bf16 whose last dimension is contiguous: pointer, token stride, head stride.  (The
+    stride of a dimension of one entry is never used; torch leaves anything there.)"""
+    if t.dtype is not _BF16:
         raise MxqBufferError("%s must be torch.bfloat16 (got %s)" % (name, t.dtype))
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise MxqBufferError("%s must be [tokens, heads, dim] as the cache has them (got %s)" % (name, tuple(t.shape)))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and d > 1:
         raise MxqBufferError("%s needs a contiguous last dimension" % name)
-    # the stride of a dimension of one entry (or of none) is never used
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+    if t.device != device:
+        raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
+    return _ptr_strided(t), (s0 if n > 1 else 0), (s1 if h > 1 else 0)
 
 
 def _ptr_strided(t):
@@ -415,55 +439,44 @@ def _ptr_strided(t):
 
 def _kv_layer(cache, head_dim, f):
     """(pages, kv_heads, page_size) of one layer of the cache."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4:
+    if cache.dtype is not _U8 or cache.dim() != 4:
         raise MxqBufferError("cache must be uint8 [pages, kv_heads, page_size / 16, unit] (got %s %s)" %
                              (cache.dtype, tuple(cache.shape)))
-    unit = kv_unit_bytes(head_dim, f)
-    if cache.shape[3] != unit:
-        raise MxqBufferError("a unit of the cache holds %d bytes, heads of %d take %d" % (cache.shape[3], head_dim, unit))
-    return cache.shape[0], cache.shape[1], 16 * cache.shape[2]
+    pages, heads, units, unit = cache.shape
+    if unit != _KV_UNIT.get((f, head_dim), unit):  # (what the table does not hold, the library refuses)
+        raise MxqBufferError("a unit of the cache holds %d bytes, heads of %d take %d" % (unit, head_dim, _KV_UNIT[f, head_dim]))
+    return pages, heads, 16 * units
 
 
 def kv_append(k, v, cache, slots, fmt, rule=CEIL, g_k=None, g_v=None, stream=None):
     """Quantize k, v [tokens, kv_heads, dim] bf16 (strided) into one layer of the cache at `slots` (int32,
     page * page_size + offset; negative: skipped)."""
-    f = _fmt(fmt)
-    T, H, D = k.shape if k.dim() == 3 else (0, 0, 0)
-    ks = _strided(k, "k")
+    f, dev = _fmt(fmt), cache.device
+    if k.dim() != 3 or k.shape != v.shape:
+        raise MxqBufferError("k and v must be [tokens, kv_heads, dim] both (got %s, %s)" % (tuple(k.shape), tuple(v.shape)))
+    T, H, D = k.shape
     pages, heads, page_size = _kv_layer(cache, D, f)
     if H != heads:
         raise MxqBufferError("k has %d heads, the cache %d" % (H, heads))
-    vs = _strided(v, "v", H, D)
-    if v.shape[0] != T:
-        raise MxqBufferError("k and v hold %d and %d tokens" % (T, v.shape[0]))
-    _need_ints(slots, "slots", T)
-    _need(g_k, "g_k", 4, torch.float32)
-    _need(g_v, "g_v", 4, torch.float32)
-    _same_device(cache, k=k, v=v, slots=slots, g_k=g_k, g_v=g_v)
-    with _on(cache):
-        _check(lib().mxq_kv_append(_ptr_strided(k), _ptr_strided(v), T, H, D, ks[0], ks[1], vs[0], vs[1], _ptr(slots), f,
-                                   _rule(rule), _ptr(g_k), _ptr(g_v), _ptr(cache), pages, page_size, _stream(stream)),
-               "mxq_kv_append")
+    kp, ks, kh = _rows(k, "k", dev)
+    vp, vs, vh = _rows(v, "v", dev)
+    _call("mxq_kv_append", dev, stream, kp, vp, T, H, D, ks, kh, vs, vh, _at(slots, "slots", _I32, T, dev), f, _rule(rule),
+          _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _ptr(cache), pages, page_size)
 
 
 def kv_read(cache, slots, fmt, head_dim, g_k=None, g_v=None, k_out=None, v_out=None, stream=None):
     """The tokens at `slots` of one layer of the cache as bf16 (k, v), each [tokens, kv_heads, head_dim]."""
-    f = _fmt(fmt)
+    f, dev = _fmt(fmt), cache.device
     pages, H, page_size = _kv_layer(cache, head_dim, f)
-    _need_ints(slots, "slots")
     T = slots.numel()
     if k_out is None:
-        k_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+        k_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
     if v_out is None:
-        v_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
-    _need(k_out, "k_out", 2 * T * H * head_dim, torch.bfloat16)
-    _need(v_out, "v_out", 2 * T * H * head_dim, torch.bfloat16)
-    _need(g_k, "g_k", 4, torch.float32)
-    _need(g_v, "g_v", 4, torch.float32)
-    _same_device(cache, slots=slots, k_out=k_out, v_out=v_out, g_k=g_k, g_v=g_v)
-    with _on(cache):
-        _check(lib().mxq_kv_read(_ptr(cache), pages, page_size, H, head_dim, f, _ptr(slots), T, _ptr(g_k), _ptr(g_v),
-                                 _ptr(k_out), _ptr(v_out), _stream(stream)), "mxq_kv_read")
+        v_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
+    n = T * H * head_dim
+    _call("mxq_kv_read", dev, stream, _ptr(cache), pages, page_size, H, head_dim, f, _at(slots, "slots", _I32, T, dev), T,
+          _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _at(k_out, "k_out", _BF16, n, dev),
+          _at(v_out, "v_out", _BF16, n, dev))
     return k_out, v_out
 
 
@@ -480,109 +493,89 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     block_table int32 [batch, pages], kv_lens int32 [batch] (the query tokens included), q_start int32
     [batch + 1] (None: max_q rows a sequence).  scale: dim ** -0.5 by default.  Rows that see no token
     get zeros and -inf; rows of no sequence are left as they were."""
-    f = _fmt(fmt)
-    rows, heads, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    qs = _strided(q, "q")
+    f, dev = _fmt(fmt), q.device
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise MxqBufferError("q must be [rows, heads, dim] and block_table [batch, pages] (got %s, %s)" %
+                             (tuple(q.shape), tuple(block_table.shape)))
+    rows, heads, D = q.shape
     pages, kv_heads, page_size = _kv_layer(cache, D, f)
-    if block_table.dim() != 2 or (block_table.numel() and block_table.stride(1) != 1 and block_table.shape[1] > 1):
-        raise MxqBufferError("block_table must be [batch, pages] with contiguous rows")
+    qp, qs, qh = _rows(q, "q", dev)
     batch, cols = block_table.shape
-    _need_ints(block_table, "block_table")
-    _need_ints(kv_lens, "kv_lens", batch)
-    _need_ints(q_start, "q_start", batch + 1)
-    ot = OUT_FP32 if (out.dtype if out is not None else out_dtype) == torch.float32 else OUT_BF16
+    t0, t1 = block_table.stride()
+    if (t1 != 1 and cols > 1) or block_table.dtype is not _I32 or block_table.device != dev or cache.device != dev:
+        raise MxqBufferError("block_table must be torch.int32 [batch, pages] with contiguous rows, on the call's device")
     if out is None:
-        out = torch.empty((rows, heads, D), dtype=out_dtype, device=q.device)
+        out = torch.empty((rows, heads, D), dtype=out_dtype, device=dev)
+    dtype = out.dtype
+    if dtype is not _F32 and dtype is not _BF16:
+        raise MxqBufferError("out must be torch.bfloat16 or torch.float32 (got %s)" % dtype)
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-    _need(out, "out", rows * heads * D * (4 if ot == OUT_FP32 else 2), torch.float32 if ot == OUT_FP32 else torch.bfloat16)
-    _need(lse, "lse", 4 * rows * heads, torch.float32)
-    _need(g_k, "g_k", 4, torch.float32)
-    _need(g_v, "g_v", 4, torch.float32)
-    _same_device(q, cache=cache, block_table=block_table, kv_lens=kv_lens, q_start=q_start, g_k=g_k, g_v=g_v, out=out,
-                 lse=lse, workspace=workspace)
-    with _on(q):
-        if workspace is None:
-            workspace = torch.empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), dtype=torch.uint8,
-                                    device=q.device)
-        stride = block_table.stride(0) if batch > 1 else max(cols, 1)
-        _check(lib().mxq_kv_attention(_ptr_strided(q), rows, qs[0], qs[1], _ptr(cache), pages, page_size, heads, kv_heads, D,
-                                      f, _ptr_strided(block_table), stride, cols, _ptr(kv_lens), batch, _ptr(q_start),
-                                      max_q, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _ptr(g_k),
-                                      _ptr(g_v), ot, _ptr(out), _ptr(lse), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_attention")
+        lse = torch.empty((rows, heads), dtype=_F32, device=dev)
+    if workspace is None:
+        with _on(q):
+            workspace = torch.empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), dtype=_U8, device=dev)
+    _call("mxq_kv_attention", dev, stream, qp, rows, qs, qh, _ptr(cache), pages, page_size, heads, kv_heads, D, f,
+          _ptr_strided(block_table), t0 if batch > 1 else max(cols, 1), cols, _at(kv_lens, "kv_lens", _I32, batch, dev),
+          batch, _at(q_start, "q_start", _I32, batch + 1, dev), max_q, D ** -0.5 if scale is None else scale, causal, window,
+          _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), dtype is _F32,
+          _at(out, "out", dtype, rows * heads * D, dev), _at(lse, "lse", _F32, rows * heads, dev),
+          _at(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size())
     return out, lse
 
 
-def _pages_state(block_table, kv_lens, refs, info):
-    """Checks the page state and returns (rows, stride, columns, info tensor)."""
+def _pages_args(block_table, kv_lens, refs, info, page_size):
+    """Checks the page state; the arguments that all page calls share, and info."""
+    dev = refs.device
     if block_table.dim() != 2 or not block_table.is_contiguous():
         raise MxqBufferError("block_table must be a contiguous [rows, pages] tensor")
-    _need_ints(block_table, "block_table")
-    _need_ints(kv_lens, "kv_lens", block_table.shape[0])
-    _need_ints(refs, "refs", 1)
+    rows, cols = block_table.shape
     if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=refs.device)
-    _need_ints(info, "info", 2)
-    return block_table.shape[0], block_table.shape[1], info
+        info = torch.empty(2, dtype=_I32, device=dev)
+    return (_at(block_table, "block_table", _I32, 0, dev), rows, cols, cols, _at(kv_lens, "kv_lens", _I32, rows, dev),
+            _at(refs, "refs", _I32, 1, dev), refs.numel(), page_size), info
 
 
-def _kv_layers(cache, page_size, num_pages):
-    """(layers, layer stride, bytes of a page) of a cache of one or more layers."""
-    if cache.dtype != torch.uint8 or cache.dim() not in (4, 5) or not cache.is_contiguous():
+def _kv_layers(cache, page_size, num_pages, dev):
+    """Pointer, layers, layer stride and bytes of a page of a cache of one or more layers."""
+    if cache.dtype is not _U8 or cache.dim() not in (4, 5):
         raise MxqBufferError("cache must be a contiguous uint8 [(layers,) pages, kv_heads, page_size / 16, unit] tensor")
     layers = cache.shape[0] if cache.dim() == 5 else 1
     pages, heads, units, unit = cache.shape[-4:]
     if pages < num_pages or 16 * units != page_size:
         raise MxqBufferError("the cache has %d pages of %d tokens, the call is for %d of %d" %
                              (pages, 16 * units, num_pages, page_size))
-    return layers, pages * heads * units * unit, heads * units * unit
+    return _at(cache, "cache", _U8, 0, dev), layers, pages * heads * units * unit, heads * units * unit
 
 
 def kv_reserve(seqs, add, block_table, kv_lens, refs, cache, page_size, slots=None, info=None, workspace=None, stream=None):
     """Room for add[i] more tokens in row seqs[i] (int32 each); `cache` is [pages, ...] or [layers, pages, ...].
     slots receives the new tokens' slots, then -1.  Returns info (int32[2]: status, pages taken)."""
-    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
-    n, num_pages = seqs.numel(), refs.numel()
-    _need_ints(seqs, "seqs")
-    _need_ints(add, "add", n)
-    _need_ints(slots, "slots")
-    layers, stride, page_bytes = _kv_layers(cache, page_size, num_pages)
-    _same_device(refs, seqs=seqs, add=add, block_table=block_table, kv_lens=kv_lens, cache=cache, slots=slots, info=info,
-                 workspace=workspace)
-    with _on(refs):
-        if workspace is None:
-            workspace = torch.empty(max(lib().mxq_kv_reserve_workspace_size(n), 16), dtype=torch.uint8, device=refs.device)
-        _check(lib().mxq_kv_reserve(_ptr(seqs), _ptr(add), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens), _ptr(refs),
-                                    num_pages, page_size, _ptr(cache), layers, stride, page_bytes, _ptr(slots),
-                                    0 if slots is None else slots.numel(), _ptr(info), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_reserve")
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    n, dev = seqs.numel(), refs.device
+    layers = _kv_layers(cache, page_size, refs.numel(), dev)
+    if workspace is None:
+        workspace = torch.empty(16 + 8 * n, dtype=_U8, device=dev)
+    _call("mxq_kv_reserve", dev, stream, _at(seqs, "seqs", _I32, n, dev), _at(add, "add", _I32, n, dev), n, *state, *layers,
+          _at(slots, "slots", _I32, 0, dev), 0 if slots is None else slots.numel(), _at(info, "info", _I32, 2, dev),
+          _at(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size())
     return info
 
 
 def kv_fork(parents, children, block_table, kv_lens, refs, page_size, info=None, stream=None):
     """Empty row children[i] becomes a copy of row parents[i] that shares its pages.  Returns info."""
-    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
-    n = parents.numel()
-    _need_ints(parents, "parents")
-    _need_ints(children, "children", n)
-    _same_device(refs, parents=parents, children=children, block_table=block_table, kv_lens=kv_lens, info=info)
-    with _on(refs):
-        _check(lib().mxq_kv_fork(_ptr(parents), _ptr(children), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens),
-                                 _ptr(refs), refs.numel(), page_size, _ptr(info), _stream(stream)), "mxq_kv_fork")
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    n, dev = parents.numel(), refs.device
+    _call("mxq_kv_fork", dev, stream, _at(parents, "parents", _I32, n, dev), _at(children, "children", _I32, n, dev), n,
+          *state, _at(info, "info", _I32, 2, dev))
     return info
 
 
 def kv_truncate(seqs, new_lens, block_table, kv_lens, refs, page_size, info=None, stream=None):
     """Cut row seqs[i] to new_lens[i] tokens (0 frees it).  Returns info."""
-    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
-    n = seqs.numel()
-    _need_ints(seqs, "seqs")
-    _need_ints(new_lens, "new_lens", n)
-    _same_device(refs, seqs=seqs, new_lens=new_lens, block_table=block_table, kv_lens=kv_lens, info=info)
-    with _on(refs):
-        _check(lib().mxq_kv_truncate(_ptr(seqs), _ptr(new_lens), n, _ptr(block_table), rows, cols, cols, _ptr(kv_lens),
-                                     _ptr(refs), refs.numel(), page_size, _ptr(info), _stream(stream)), "mxq_kv_truncate")
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    n, dev = seqs.numel(), refs.device
+    _call("mxq_kv_truncate", dev, stream, _at(seqs, "seqs", _I32, n, dev), _at(new_lens, "new_lens", _I32, n, dev), n, *state,
+          _at(info, "info", _I32, 2, dev))
     return info
 
 
@@ -593,14 +586,11 @@ def kv_compact_workspace(num_pages):
 
 def kv_compact(block_table, kv_lens, refs, cache, page_size, info=None, workspace=None, stream=None):
     """Pack the pages in use to the front of the cache.  Returns info (int32[2]: 0, pages in use)."""
-    rows, cols, info = _pages_state(block_table, kv_lens, refs, info)
-    num_pages = refs.numel()
-    layers, stride, page_bytes = _kv_layers(cache, page_size, num_pages)
-    _same_device(refs, block_table=block_table, kv_lens=kv_lens, cache=cache, info=info, workspace=workspace)
-    with _on(refs):
-        if workspace is None:
-            workspace = torch.empty(kv_compact_workspace(num_pages), dtype=torch.uint8, device=refs.device)
-        _check(lib().mxq_kv_compact(_ptr(block_table), rows, cols, cols, _ptr(kv_lens), _ptr(refs), num_pages, page_size,
-                                    _ptr(cache), layers, stride, page_bytes, _ptr(info), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)), "mxq_kv_compact")
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    dev = refs.device
+    layers = _kv_layers(cache, page_size, refs.numel(), dev)
+    if workspace is None:
+        workspace = torch.empty(kv_compact_workspace(refs.numel()), dtype=_U8, device=dev)
+    _call("mxq_kv_compact", dev, stream, *state, *layers, _at(info, "info", _I32, 2, dev),
+          _at(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size())
     return info
