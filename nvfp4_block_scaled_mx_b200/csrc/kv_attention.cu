@@ -22,8 +22,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "kv.cuh"
-#include "kv_internal.h"
+#include "kv_attn_common.cuh"
 #include "mxq_internal.h"
 
 namespace mxq {
@@ -31,22 +30,13 @@ namespace {
 
 constexpr int kWarps = 4;                     // warps that compute; one more feeds them
 constexpr int kThreads = (kWarps + 1) * 32;
+#ifndef C_NTMAX
+#define C_NTMAX 3
+#endif
 #ifndef C_MINT
 #define C_MINT 4
 #endif
 constexpr int kMinTiles = C_MINT;  // token tiles a CTA gets at least
-constexpr float kNegMax = -3.402823466e38f;
-
-// A run of token tiles of one row tile and kv head, as the feeding warp describes it.
-struct Segment {
-    int count;                     // token tiles; -1: no more work
-    uint32_t base;                 // tiles in front of it in the CTA's ring
-    int pos0;                      // first token of its first tile
-    int seen0, seen1, all0, all1;  // tokens that any row sees, and that all rows see
-    int q0, row0, rows, head;      // first query row of the sequence, row tile, its rows, kv head
-    int begins, whole;             // has the row tile's first token tile; has all of them
-    int parts;                     // if it begins but is not whole: CTAs that have a part
-};
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -60,7 +50,7 @@ struct Cfg {
     static constexpr int Q_BYTES = NT * KS * 32 * 8;
     static constexpr int RED = kWarps * ROWS * OSTRIDE * 4;
     // CTAs an SM holds, by registers (an accumulator of 4 NT KS a lane), and what is left of its shared memory
-    static constexpr int CTAS = NT * KS <= 8 ? 3 : NT * KS <= 16 ? 2 : 1;
+    static constexpr int CTAS = NT * KS <= 8 ? 3 : NT * KS <= 24 ? 2 : 1;
     static constexpr int BUDGET = (227 / CTAS - 1) * 1024 - 1024;
     static constexpr int FIXED = 2 * Q_BYTES + RED + 2 * (ROWS * 12 + 64) + kWarps * ROWS * 8 + 64;
     static constexpr int FIT = (BUDGET - FIXED) / (TILE_BYTES + 16);
@@ -77,230 +67,6 @@ struct Cfg {
     static_assert(sizeof(Segment) <= 64, "segment note");
     static constexpr float SHIFT = FMT == MXQ_NVFP4 ? 7.0f : 4.0f;  // log2 of what P is multiplied by
 };
-
-// One sequence as the kernels see it.
-struct Seq {
-    int kv, q0, qn;  // tokens in the cache, first query row, query rows
-};
-
-__device__ __noinline__ Seq load_seq(const KvAttnArgs& a, int b) {
-    Seq s;
-    s.kv = a.lens[b];
-    if (s.kv > a.max_len) {
-        kv_status(a.status, kStatusKvLen);
-        s.kv = a.max_len;
-    }
-    s.kv = max(s.kv, 0);
-    if (a.q_start) {
-        const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
-        s.q0 = q0;
-        s.qn = max(q1 - q0, 0);
-        if (q0 < 0 || q1 > a.rows_total || s.qn > a.max_q) {
-            kv_status(a.status, kStatusKvRows);
-            s.q0 = s.qn = 0;
-        }
-    } else {
-        s.q0 = b * a.max_q;
-        s.qn = a.max_q;
-    }
-    return s;
-}
-
-// Tokens [first, end) that row r of the sequence sees.
-__device__ __forceinline__ void row_span(const KvAttnArgs& a, const Seq& s, int r, int& first, int& end) {
-    const int seen = s.kv - s.qn + (a.max_q == 1 ? 0 : r / a.group) + 1;
-    end = a.causal ? max(seen, 0) : s.kv;
-    first = a.window > 0 ? max(seen - a.window, 0) : 0;
-}
-
-// Token tiles [t0, t0 + n) of a row tile; an empty one counts as one tile, so that its rows are written.
-template <int TILE, int ROWS>
-__device__ __forceinline__ int tile_span(const KvAttnArgs& a, const Seq& s, int qt, int& t0) {
-    const int rows = s.qn * a.group, r0 = qt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
-    int first, end, skip;
-    row_span(a, s, r0, first, skip);
-    row_span(a, s, r1, skip, end);
-    t0 = first / TILE;
-    return max((end + TILE - 1) / TILE - t0, 1);
-}
-
-template <int TILE, int ROWS>
-__device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
-    int64_t n = 0;
-    const int tiles = (s.qn * a.group + ROWS - 1) / ROWS;
-#pragma unroll 1
-    for (int qt = 0; qt < tiles; ++qt) {
-        int t0;
-        n += tile_span<TILE, ROWS>(a, s, qt, t0);
-    }
-    return n * a.kv_heads;
-}
-
-// n / d for quotients below 2^20: a float quotient, corrected by at most a step or two (a 64-bit division
-// is many more instructions, and this code runs once per segment from a cold instruction cache).
-__device__ __forceinline__ int div_small(int64_t n, int64_t d, int64_t& r) {
-    int q = static_cast<int>(__fdividef(static_cast<float>(n), static_cast<float>(d)));
-    r = n - q * d;
-    while (r < 0) r += d, --q;
-    while (r >= d) r -= d, ++q;
-    return q;
-}
-
-// The cut of the batch's work, in token tiles: CTA c takes [c per, (c + 1) per).  Whole warp, every warp
-// for itself; `at` is this CTA's first tile, b and off the sequence that holds it and its place there.
-struct Plan {
-    int64_t work, per, at, off;
-    int b;
-};
-
-template <int TILE, int ROWS>
-__device__ __forceinline__ Plan make_plan(const KvAttnArgs& a) {
-    const int lane = threadIdx.x & 31;
-    Plan p;
-    int64_t own = 0, sum = 0;  // of the last 32 sequences: the lane's, and the inclusive scan over the lanes
-    p.work = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
-        sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
-        }
-        p.work += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    // any share that covers the work will do: the quotient in floats, rounded up past its error of 2^-22
-    p.per = static_cast<int64_t>(static_cast<float>(p.work) * a.inv_grid * 1.000001f) + 1;
-    if (p.per < kMinTiles) p.per = kMinTiles;
-    p.at = p.per * blockIdx.x;
-    p.b = a.batch;
-    p.off = 0;
-    if (p.at >= p.work) return p;
-    int64_t base = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        if (a.batch > 32) {
-            own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
-            sum = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
-            }
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + sum > p.at);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            p.off = p.at - base - __shfl_sync(0xffffffffu, sum - own, l);
-            p.b = b0 + l;
-            break;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    return p;
-}
-
-// What the join kernel needs to know of a row tile whose first part CTA c has; parts = 0: there is none.
-struct Split {
-    int parts, q0, row0, rows, head, pad[3];
-};
-
-// ------------------------------------------------------------------------------ instructions
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same from zero.
-__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// 8 E2M1 codes as 4 f16x2: byte i of w becomes o[i], its low nibble in the low half.
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&o)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t h) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(h));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// N bytes (4, 8 or 16) of shared memory as words.
-template <int N>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N / 4]) {
-    if constexpr (N == 4) {
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
-    } else if constexpr (N == 8) {
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
-    } else {
-        static_assert(N == 16, "bytes");
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "r"(addr));
-    }
-}
-
-// 2^e as fp32 for e in [-252, 127], as a product of two normal factors where one would not do.
-__device__ __forceinline__ float scale_pow2(float x, int e) {
-    if (e < -126) {
-        x *= __uint_as_float(1u << 23);  // 2^-126
-        e += 126;
-    }
-    return x * __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
-}
-
-// mbar_wait_warp with the waiting loop out of line: there are many waits, and their code counts.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* status, int where) {
-    return mbar_wait(bar, parity, status, where);
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status, int where) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, wait_slow(bar, parity, status, where));
-    else ok = true;
-    return ok;
-}
 
 // --------------------------------------------------------------------------------- warp state
 
@@ -427,11 +193,6 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
             }
         }
     }
-}
-
-// Mask of the scale bytes of tokens pos (even bytes) and pos + 1 that lie in [first, end).
-__device__ __forceinline__ uint32_t pair_mask(int pos, int first, int end) {
-    return (pos >= first && pos < end ? 0x00FF00FFu : 0u) | (pos + 1 >= first && pos + 1 < end ? 0xFF00FF00u : 0u);
 }
 
 // One token tile: scores, softmax update, O update.  pos0 is the tile's first token; MASK: some row does
@@ -626,17 +387,6 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
 
 // ------------------------------------------------------------------------------------- kernel
 
-// Writes four neighbouring channels of a row.
-__device__ __forceinline__ void put4(const KvAttnArgs& a, int64_t at, float x, float y, float z, float w) {
-    if (a.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(x, y, z, w);
-    } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(x, y), hi = __floats2bfloat162_rn(z, w);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    }
-}
-
 // The feeding warp: walks the CTA's work, notes each segment and its Q operands (two buffers), and keeps
 // the ring of token tiles full, so that the computing warps never wait for an index or a query.
 template <int FMT, int D, int NT>
@@ -649,7 +399,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     uint64_t* seg_full = empty + C::STAGES;
     uint64_t* seg_empty = seg_full + 2;
 
-    const Plan plan = make_plan<C::TILE, C::ROWS>(a);
+    const Plan plan = make_plan<C::TILE, C::ROWS>(a, kMinTiles);
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
@@ -963,116 +713,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
     }
 }
 
-// Joins the parts of the row tiles that several CTAs worked on, in CTA order.  Every block gathers the
-// list of those from all CTAs' notes; its items are (row tile, slice of 16 channels).  Latency is all
-// there is to it: the parts of an item are split among PG groups of threads, each of which has the loads
-// of BATCH parts in flight, so that 56 parts (a batch of one on all SMs) take one round trip.
-constexpr int kJoinThreads = 256;
-constexpr int kMaxGrid = 1024;
-
-// Adds (m2, l2, v2) to the running (m, l, v): sums relative to 2^m.
-__device__ __forceinline__ void join_add(float& m, float& l, float4& v, float m2, float l2, const float4& v2) {
-    const float top = fmaxf(m, m2), f = ex2(m - top), f2 = ex2(m2 - top);
-    m = top;
-    l = l * f + l2 * f2;
-    v.x = v.x * f + v2.x * f2;
-    v.y = v.y * f + v2.y * f2;
-    v.z = v.z * f + v2.z * f2;
-    v.w = v.w * f + v2.w * f2;
-}
-
-template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const __grid_constant__ KvAttnArgs a, int grid) {
-    using C = Cfg<FMT, D, NT>;
-    constexpr int SLICE = 16, SLICES = D / SLICE, ELEMS = C::ROWS * SLICE / 4, PG = kJoinThreads / ELEMS, BATCH = 8;
-    __shared__ uint32_t has[kMaxGrid / 32];
-    __shared__ int list[kMaxGrid], count;
-    __shared__ float2 mls[PG][ELEMS];
-    __shared__ float4 vs[PG][ELEMS];
-    pdl_launch_dependents();
-    pdl_wait();
-    const Split* splits = reinterpret_cast<const Split*>(a.partial);
-    const float* partials = a.partial + grid * (sizeof(Split) / 4);
-    const float gv = FMT == MXQ_NVFP4 ? *a.g_v : 1.0f;
-    // the list is the same in every block: CTAs in order, placed by counting those in front
-    uint32_t mask[kMaxGrid / kJoinThreads];
-#pragma unroll
-    for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
-        const int c = i * kJoinThreads + threadIdx.x;
-        mask[i] = c < grid ? splits[c].parts : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
-        const uint32_t m = __ballot_sync(0xffffffffu, mask[i] != 0);
-        if ((threadIdx.x & 31) == 0) has[(i * kJoinThreads + threadIdx.x) / 32] = m;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        static_assert(kMaxGrid == 32 * 32, "one word of the mask a lane");
-        uint32_t m = has[threadIdx.x];
-        int before = __popc(m);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, before, o);
-            if (static_cast<int>(threadIdx.x) >= o) before += x;
-        }
-        if (threadIdx.x == 31) count = before;
-        before -= __popc(m);
-        for (; m; m &= m - 1) list[before++] = threadIdx.x * 32 + __ffs(m) - 1;
-    }
-    __syncthreads();
-    constexpr int PART = C::ROWS * (D + 2);
-    const int pg = threadIdx.x / ELEMS, e = threadIdx.x % ELEMS, r = e / (SLICE / 4);
-#pragma unroll 1
-    for (int i = blockIdx.x; i < count * SLICES; i += gridDim.x) {
-        const int c = list[i / SLICES], d = i % SLICES * SLICE + e % (SLICE / 4) * 4;
-        const Split s = splits[c];
-        // slot 1 of the first CTA, slot 0 of the others
-        const float* first = partials + (static_cast<int64_t>(c) * 2 + 1) * PART;
-        float m = kNegMax, l = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-        for (int k0 = pg; k0 < s.parts; k0 += PG * BATCH) {
-            float2 z[BATCH];
-            float4 x[BATCH];
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                const int k = k0 + j * PG;
-                const float* at = first + (k == 0 ? 0 : (2 * k - 1) * static_cast<int64_t>(PART));
-                z[j] = make_float2(kNegMax, 0.0f);
-                x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (k < s.parts) {
-                    z[j] = *reinterpret_cast<const float2*>(at + C::ROWS * D + 2 * r);
-                    x[j] = *reinterpret_cast<const float4*>(at + r * D + d);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) join_add(m, l, v, z[j].x, z[j].y, x[j]);
-        }
-        mls[pg][e] = make_float2(m, l);
-        vs[pg][e] = v;
-        __syncthreads();
-        if (pg == 0 && r < s.rows) {
-#pragma unroll
-            for (int k = 1; k < PG; ++k) join_add(m, l, v, mls[k][e].x, mls[k][e].y, vs[k][e]);
-            const int row = s.row0 + r;
-            const int64_t o = static_cast<int64_t>(s.q0 + row / a.group) * a.heads + s.head * a.group + row % a.group;
-            const float inv = gv * (l > 0.0f ? 1.0f / l : l);  // l is 0 (no token) or not a number
-            put4(a, o * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            if (a.lse && d == 0)
-                a.lse[o] = l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
-        }
-        __syncthreads();
-    }
-}
-
 // --------------------------------------------------------------------------------------- host
 
 // n-tiles of eight rows: as few as hold a sequence's rows, at most what the registers hold.
 int n_tiles(int64_t rows, int D) {
     if (rows <= 8) return 1;
     if (rows <= 16 || D == 256) return 2;
-    return 4;
+    return C_NTMAX;
 }
 
 constexpr int kMaxCtasPerSm = 4;
@@ -1081,7 +728,7 @@ template <int FMT, int D, int NT>
 int run(KvAttnArgs& a, cudaStream_t st) {
     using C = Cfg<FMT, D, NT>;
     auto kernel = kv_attention_kernel<FMT, D, NT>;
-    auto join = kv_attention_join_kernel<FMT, D, NT>;
+    auto join = kv_attention_join_kernel<FMT, D, C::ROWS>;
     // resident CTAs of an SM, asked once per device (0: not asked yet)
     static std::atomic<int> known[64];
     int dev = -1;
@@ -1115,8 +762,8 @@ int run(KvAttnArgs& a, cudaStream_t st) {
 
 template <int FMT>
 int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
-    if (D == 64) return nt == 1 ? run<FMT, 64, 1>(a, st) : nt == 2 ? run<FMT, 64, 2>(a, st) : run<FMT, 64, 4>(a, st);
-    if (D == 128) return nt == 1 ? run<FMT, 128, 1>(a, st) : nt == 2 ? run<FMT, 128, 2>(a, st) : run<FMT, 128, 4>(a, st);
+    if (D == 64) return nt == 1 ? run<FMT, 64, 1>(a, st) : nt == 2 ? run<FMT, 64, 2>(a, st) : run<FMT, 64, C_NTMAX>(a, st);
+    if (D == 128) return nt == 1 ? run<FMT, 128, 1>(a, st) : nt == 2 ? run<FMT, 128, 2>(a, st) : run<FMT, 128, C_NTMAX>(a, st);
     return nt == 1 ? run<FMT, 256, 1>(a, st) : run<FMT, 256, 2>(a, st);
 }
 
@@ -1124,12 +771,16 @@ int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
 
 size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_heads, int D) {
     (void)batch;
-    const int rows = 8 * n_tiles(max_q * (heads / kv_heads), D);
-    return static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * rows * (D + 2) * 4 + sizeof(Split));
+    const int64_t rows = max_q * (heads / kv_heads);
+    const size_t here = static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * 8 * n_tiles(rows, D) * (D + 2) * 4 + sizeof(Split));
+    const size_t there = static_cast<size_t>(sm_count()) * (2 * kv_rows_tile(rows) * (D + 2) * 4 + sizeof(Split));
+    return rows > 8 && D <= 128 ? std::max(here, there) : here;
 }
 
 int launch_kv_attention(int fmt, int D, KvAttnArgs& a, cudaStream_t st) {
-    const int nt = n_tiles(static_cast<int64_t>(a.max_q) * a.group, D);
+    const int64_t rows = static_cast<int64_t>(a.max_q) * a.group;
+    if (rows > 8 && fmt == MXQ_NVFP4 && D <= 128) return launch_kv_attention_rows(D, a, st);
+    const int nt = n_tiles(rows, D);
     return fmt == MXQ_NVFP4 ? run_dim<MXQ_NVFP4>(D, nt, a, st) : run_dim<MXQ_MXFP4>(D, nt, a, st);
 }
 

@@ -1,0 +1,743 @@
+// kv_attention_rows.cu -- attention over the paged 4-bit cache for sequences with more than eight rows
+// (query token x query head of a kv head's group): drafted tokens, chunks of a prefill.
+//
+// With many rows the tensor work counts, so it runs on tcgen05 (kind::f16, fp32 accumulators in TMEM), one
+// CTA per SM, tiles of 128 tokens:
+//   S = Q K^T   Q [128 rows x D] in TMEM (the A operand, written once per segment), K decoded into shared
+//               memory as f16 (codes times E4M3 scale, exact), 128-byte swizzle;
+//   P = 2^(s - base), f16, in TMEM; one thread has one row, so the softmax needs no shuffles;
+//   O += P V    V decoded as f16 into shared memory transposed ([channel][token]).
+// Roles: two groups of 4 softmax warps (their TMEM lanes are the rows) that take the tiles in turn, each with
+// its own S and O, so that one group's exponentials run beside the other's products; 4 warps that decode K
+// (32 tokens of a tile each) and 8 that decode V (16 tokens); one warp that feeds raw tiles by bulk copies;
+// one that issues the MMAs.  P takes the place of S's first half: chunk by chunk of 32 tokens the scores are
+// read, and their probabilities written where scores have been read already.
+// QUAD (up to 32 rows): the rows stand four times in the lanes, and each softmax warp takes 32 of the tile's
+// 128 tokens, the others' P columns being zero: the four partial results join at the end, like CTAs' parts.
+// The base of a row follows its maximum only when a probability would pass 2^15 (f16 ends at 2^16); O and
+// the tile's earlier P are rescaled in TMEM then.  Work is cut over the CTAs as in kv_attention.cu, with the
+// same join kernel.
+#include <algorithm>
+#include <atomic>
+
+#include "kv_attn_common.cuh"
+#include "mxq_internal.h"
+
+namespace mxq {
+namespace {
+
+constexpr int kSoftWarps = 8, kKeyWarps = 4, kValueWarps = 8, kDecWarps = kKeyWarps + kValueWarps;
+constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
+constexpr int kRowThreads = (kMmaWarp + 1) * 32;
+constexpr int kTokens = 128;  // of a tile
+constexpr int kMinRowTiles = 2;
+constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^7; above 2^15 it is raised
+
+template <int FMT, int D, bool QUAD>
+struct RCfg {
+    using U = KvUnit<FMT, D>;
+    static constexpr int ROWS = QUAD ? 32 : 128;
+    static constexpr int UNITS = kTokens / 16;
+    static constexpr int RAW = UNITS * U::BYTES;
+    static constexpr int STAGES = 3;
+    static constexpr int K16 = kTokens * D * 2, V16 = kTokens * D * 2, Q16 = 128 * D * 2;  // bytes of an operand
+    static constexpr int OFF_K = 0;  // 1024-byte aligned, as the others
+    static constexpr int OFF_V = OFF_K + 2 * K16;
+    static constexpr int OFF_Q = OFF_V + 2 * V16;  // QUAD: at a segment's end also [4][32][MERGE] floats
+    static constexpr int MERGE = D == 128 ? 33 : 17;  // a column slice and a skew
+    static_assert(4 * 32 * MERGE * 4 <= Q16, "merge buffer");
+    static constexpr int OFF_RAW = OFF_Q + Q16;
+    static constexpr int OFF_ML = OFF_RAW + STAGES * RAW;  // [2 groups][128 lanes] (base, l)
+    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // scale of each row's scores
+    static constexpr int OFF_SEG = OFF_QS + 128 * 4;
+    static constexpr int OFF_BAR = OFF_SEG + 2 * 64;
+    static constexpr int NBARS = 2 * STAGES + 10 + 1 + 4;
+    static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
+    static constexpr int BYTES = OFF_TMEM + 16 + 1024;  // and the alignment
+    static constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each: S 128 columns, O D columns
+};
+
+struct RowBars {
+    uint64_t *raw_full, *raw_empty, *kf, *vf, *sf, *pf, *od, *qf, *seg_full, *seg_empty;
+    __device__ __forceinline__ RowBars(uint8_t* at, int stages) {
+        uint64_t* b = reinterpret_cast<uint64_t*>(at);
+        raw_full = b, raw_empty = b + stages, b += 2 * stages;
+        // of tile n, at n & 1: K and V decoded, S done (K may be overwritten), P written, O done (V, P may be)
+        kf = b, vf = b + 2, sf = b + 4, pf = b + 6, od = b + 8, b += 10;
+        qf = b, b += 1;
+        seg_full = b, seg_empty = b + 2;
+    }
+};
+
+// Feeds raw tiles (whole warp): eight lanes have a unit each; neighbouring units of a page go as one copy.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar) {
+    using C = RCfg<FMT, D, QUAD>;
+    using U = typename C::U;
+    const int lane = threadIdx.x & 31;
+    const Plan plan = make_plan<kTokens, C::ROWS>(a, kMinRowTiles);
+    if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
+    int64_t at = plan.at, off = plan.off;
+    const int64_t stop = min(at + plan.per, plan.work);
+    int b = plan.b, qt = 0;
+    Seq s = {};
+    if (at < stop) s = load_seq(a, b);
+    uint32_t tiles = 0;
+#pragma unroll 1
+    for (uint32_t nseg = 0;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        Segment* note = reinterpret_cast<Segment*>(smem + C::OFF_SEG + buf * 64);
+        const bool more = at < stop;
+        int t0 = 0, n = 1;
+#pragma unroll 1
+        while (more) {
+            if (qt * C::ROWS >= s.qn * a.group) {
+                s = load_seq(a, ++b);
+                qt = 0;
+                continue;
+            }
+            n = tile_span<kTokens, C::ROWS>(a, s, qt, t0);
+            if (off < static_cast<int64_t>(n) * a.kv_heads) break;
+            off -= static_cast<int64_t>(n) * a.kv_heads;
+            ++qt;
+        }
+        if (!wait_warp(&bar.seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x51)) return;
+        if (!more) {
+            if (lane == 0) {
+                note->count = -1;
+                mbar_arrive(&bar.seg_full[buf]);
+            }
+            return;
+        }
+        int64_t from64;
+        const int head = div_small(off, n, from64), from = static_cast<int>(from64);
+        const int count = static_cast<int>(min(static_cast<int64_t>(n - from), stop - at));
+        const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.qn * a.group - row0);
+        int seen0, seen1, all0, all1;
+        row_span(a, s, row0, seen0, all1);
+        row_span(a, s, row0 + rows - 1, all0, seen1);
+        if (lane == 0) {
+            note->count = count;
+            note->base = tiles;
+            note->pos0 = (t0 + from) * kTokens;
+            note->seen0 = seen0, note->seen1 = seen1, note->all0 = all0, note->all1 = all1;
+            note->q0 = s.q0, note->row0 = row0, note->rows = rows, note->head = head;
+            note->kv = s.kv, note->qn = s.qn;
+            note->begins = from == 0;
+            note->whole = from == 0 && count == n;
+            int64_t rest;
+            note->parts = from == 0 ? div_small(at + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
+            mbar_arrive(&bar.seg_full[buf]);
+        }
+        const int first_unit = (t0 + from) * C::UNITS;
+        const int units_end = min((seen1 + 15) >> 4, first_unit + count * C::UNITS);  // behind the tokens pages may not exist
+        auto source_of = [&](int i) -> int64_t {  // of the lane's unit of tile i, -1: not loaded
+            const int unit = first_unit + i * C::UNITS + lane;
+            if (lane >= C::UNITS || unit >= units_end) return -1;
+            const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));
+            const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
+            if (pg < 0 || pg >= a.num_pages) {
+                kv_status(a.status, kStatusKvPage);
+                return -1;
+            }
+            return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
+                   static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
+        };
+        int64_t next = source_of(0);
+#pragma unroll 1
+        for (int i = 0; i < count; ++i, ++tiles) {
+            const int64_t src = next;
+            next = source_of(i + 1);
+            const uint32_t slot = tiles % C::STAGES;
+            if (!wait_warp(&bar.raw_empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x52)) return;
+            const uint32_t valid = __ballot_sync(0xffffffffu, src >= 0);
+            const int64_t before = __shfl_up_sync(0xffffffffu, src, 1);
+            const bool cont = lane > 0 && src >= 0 && before >= 0 && src == before + U::BYTES;
+            const uint32_t conts = __ballot_sync(0xffffffffu, cont);
+            if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], __popc(valid) * U::BYTES);
+            __syncwarp();
+            if (src >= 0 && !cont) {
+                const int run = __ffs(~(conts >> (lane + 1)));  // this unit and those that follow it without a gap
+                bulk_load(smem + C::OFF_RAW + slot * C::RAW + lane * U::BYTES, a.cache + src, run * U::BYTES, &bar.raw_full[slot]);
+            }
+            __syncwarp();
+        }
+        at += count;
+        off += count;
+    }
+}
+
+// Issues the products (whole warp, one lane elected).
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, uint32_t tmem) {
+    using C = RCfg<FMT, D, QUAD>;
+    // kind::f16 with f16 operands (formats 0), fp32 accumulator
+    constexpr uint32_t IDESC_S = (1u << 4) | ((kTokens >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t IDESC_O = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t q = smem_u32(smem + C::OFF_Q);
+    auto product = [&](uint32_t t, bool first) -> bool {  // O += P V of tile t
+        if (!wait_warp(&bar.vf[t & 1], t >> 1 & 1u, a.status, 0x53)) return false;
+        if (!wait_warp(&bar.pf[t & 1], t >> 1 & 1u, a.status, 0x54)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+            const uint32_t v = smem_u32(smem + C::OFF_V + (t & 1) * C::V16);
+#pragma unroll
+            for (int j = 0; j < kTokens / 16; ++j)
+                mma_bf16_ts(tmem + C::O_COL + (t & 1) * D, tmem + C::S_COL + (t & 1) * 128 + j * 8,
+                            smem_desc(v + (j >> 2) * (D * 128) + (j & 3) * 32, 16, 1024, kLayoutSwizzle128B), IDESC_O,
+                            first && j == 0 ? 0u : 1u);
+            tc_commit(&bar.od[t & 1]);
+        }
+        __syncwarp();
+        return true;
+    };
+    uint32_t t = 0;
+#pragma unroll 1
+    for (uint32_t nseg = 0;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        if (!wait_warp(&bar.seg_full[buf], nseg >> 1 & 1u, a.status, 0x55)) return;
+        const int count = reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64)->count;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.seg_empty[buf]);
+        if (count < 0) return;
+        if (!wait_warp(bar.qf, nseg & 1u, a.status, 0x56)) return;
+#pragma unroll 1
+        for (int i = 0; i <= count; ++i) {
+            if (i < count) {
+                if (!wait_warp(&bar.kf[t & 1], t >> 1 & 1u, a.status, 0x57)) return;
+                // S takes the place of P of tile t - 2, whose product has to be done
+                if (t >= 2 && !wait_warp(&bar.od[t & 1], (t - 2) >> 1 & 1u, a.status, 0x58)) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t k = smem_u32(smem + C::OFF_K + (t & 1) * C::K16);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const uint32_t at = (j >> 2) * (kTokens * 128) + (j & 3) * 32;
+                        mma_bf16(tmem + C::S_COL + (t & 1) * 128, smem_desc(q + at, 16, 1024, kLayoutSwizzle128B),
+                                 smem_desc(k + at, 16, 1024, kLayoutSwizzle128B), IDESC_S, j == 0 ? 0u : 1u);
+                    }
+                    tc_commit(&bar.sf[t & 1]);
+                }
+                __syncwarp();
+            }
+            // behind the scores of the next tile, so that its softmax need not wait for this product
+            if (i > 0 && !product(t - 1, i <= 2)) return;
+            if (i < count) ++t;
+        }
+    }
+}
+
+// Keys of units u, u + 1: a lane has quarter q of token r: 32-bit words of 8 elements, 16 bytes each once
+// decoded.  Eight neighbouring lanes have four tokens and two quarters, whose chunks meet different banks.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u) {
+    using U = typename RCfg<FMT, D, QUAD>::U;
+    const int lane = threadIdx.x & 31;
+    const int r0 = (lane >> 3 & 1) * 4 + (lane >> 1 & 3), q = (lane >> 4) * 2 + (lane & 1);
+    uint32_t sc[4], w[4][U::W / 4];  // loads first: a warp's own latency is what its tile takes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t unit = raw + (u + i / 2) * U::BYTES;
+        const int r = r0 + 8 * (i & 1);
+        sc[i] = D == 128 ? ld_shared_u16(unit + U::OFF_KS + r * U::NB + 2 * q) : ld_shared_u8(unit + U::OFF_KS + r * U::NB + q);
+        lds<U::W>(unit + U::k_at(r, q, 0), w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = u * 16 + 8 * i + r0, f = e4m3x2_f16x2(sc[i]);
+#pragma unroll
+        for (int k = 0; k < U::W / 4; ++k) {
+            const uint32_t f2 = k < 2 ? prmt(f, f, 0x1010u) : prmt(f, f, 0x3232u);
+            uint32_t o[4];
+            e2m1x8(w[i][k], o);
+            const uint32_t chunk = q * (U::W / 4) + k;  // of 8 elements in the row
+            st_shared_v4(k16 + (chunk >> 3) * (kTokens * 128) + row * 128 + (((chunk & 7) ^ (r0 & 7)) << 4),
+                         make_uint4(hmul2(o[0], f2), hmul2(o[1], f2), hmul2(o[2], f2), hmul2(o[3], f2)));
+        }
+    }
+}
+
+// Values of unit u, transposed: a lane has tokens 8 h + 2 t, + 1 and channels 16 j + 2 g, + 1.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void values(uint32_t raw, uint32_t v16, int u, bool edge, int pos0, int seen0, int seen1) {
+    using U = typename RCfg<FMT, D, QUAD>::U;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t unit = raw + u * U::BYTES;
+    // channel 16 j + 2 g has swizzle row 2 g, the next one 2 g + 1, whatever j is
+    const uint32_t to = v16 + (u >> 2) * (D * 128) + 2 * g * 128 + 4 * t;
+    constexpr int PB = 2 * U::NB;
+    uint32_t sb[2][PB / 4], w[2][U::W / 4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        lds<PB>(unit + U::OFF_VS + (t + 4 * h) * PB, sb[h]);
+        lds<U::W>(unit + U::OFF_V + h * (4 * D) + lane * U::W, w[h]);
+    }
+    if (edge) {
+        // tokens that no row sees: 0, whatever the bytes are; a NaN (the quantizer writes none): the
+        // largest number, as 0 times it has to be 0 for the rows that do not see the token
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t live = pair_mask(pos0 + 16 * u + 8 * h + 2 * t, seen0, seen1);
+#pragma unroll
+            for (int i = 0; i < PB / 4; ++i) sb[h][i] = __vminu4(sb[h][i] & live & 0x7F7F7F7Fu, 0x7E7E7E7Eu);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t chunk = (u & 3) * 2 + h;  // of 8 tokens in the block of 64
+        const uint32_t at0 = to + ((chunk ^ (2 * g & 7)) << 4), at1 = to + 128 + ((chunk ^ ((2 * g + 1) & 7)) << 4);
+#pragma unroll
+        for (int wd = 0; wd < D / 64; ++wd) {
+            const uint32_t x = w[h][wd], y = w[h][D / 64 + wd];
+            uint32_t lo[4], hi[4];
+            e2m1x8((x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), lo);
+            e2m1x8((x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 4 * wd + k;
+                const uint32_t f = e4m3x2_f16x2(j & 1 ? sb[h][j >> 1] >> 16 : sb[h][j >> 1] & 0xFFFFu);
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(hmul2(lo[k], f)) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(hmul2(hi[k], f)) : "memory");
+            }
+        }
+    }
+}
+
+// Decodes tiles to f16 operands: warps 0-3 the keys of two units each, warps 4-11 the values of one.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, int warp) {
+    using C = RCfg<FMT, D, QUAD>;
+    using U = typename C::U;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (uint32_t nseg = 0;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        if (!wait_warp(&bar.seg_full[buf], nseg >> 1 & 1u, a.status, 0x59)) return;
+        const Segment& note = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
+        const int count = note.count, seen0 = note.seen0, seen1 = note.seen1, all0 = note.all0, all1 = note.all1;
+        const uint32_t base = note.base;
+        int pos0 = note.pos0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.seg_empty[buf]);
+        if (count < 0) return;
+#pragma unroll 1
+        for (int i = 0; i < count; ++i, pos0 += kTokens) {
+            const uint32_t n = base + i, slot = n % C::STAGES;
+            if (!wait_warp(&bar.raw_full[slot], n / C::STAGES & 1u, a.status, 0x5a)) return;
+            const uint32_t raw = smem_u32(smem + C::OFF_RAW + slot * C::RAW);
+            if (warp < kKeyWarps) {
+                if (!wait_warp(&bar.sf[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5b)) return;
+                keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp);
+            } else {
+                if (!wait_warp(&bar.od[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5c)) return;
+                values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
+                                     pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(warp < kKeyWarps ? &bar.kf[n & 1] : &bar.vf[n & 1]);
+                mbar_arrive(&bar.raw_empty[slot]);
+            }
+        }
+    }
+}
+
+// Softmax: a thread has one row (QUAD: one row and a quarter of each tile's tokens) in every second tile.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, uint32_t tmem) {
+    using C = RCfg<FMT, D, QUAD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
+    const int tl = quad * 32 + lane, r = QUAD ? lane : tl;          // TMEM lane, row
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad) << 21);  // the warp's 32 TMEM lanes
+    constexpr int CHUNKS = QUAD ? 1 : 4;                                // of 32 tokens
+    const int chunk0 = QUAD ? quad : 0;
+    float* merge = reinterpret_cast<float*>(smem + C::OFF_Q);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    float* partials = a.partial + gridDim.x * (sizeof(Split) / 4);
+    const float qscale = a.scale * 1.4426950408889634f * *a.g_k, gv = *a.g_v;
+    uint32_t v[32];
+#pragma unroll 1
+    for (uint32_t nseg = 0;; ++nseg) {
+        const uint32_t buf = nseg & 1u;
+        bool dead = !wait_warp(&bar.seg_full[buf], nseg >> 1 & 1u, a.status, 0x5d);
+        // one decision for all; also: the last segment's merge buffer, which Q overlies, has been read
+        if (named_barrier_or(1, kSoftWarps * 32, dead)) return;
+        const Segment note = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.seg_empty[buf]);
+        if (note.count < 0) return;
+        // Q rows: f16 times a power of two (largest element in [2^7, 2^8)).  A warp takes every eighth row,
+        // all its lanes one row at a time; QUAD: the row stands in all four groups of lanes.
+        {
+            constexpr int PER = C::ROWS / kSoftWarps, E = D / 32;  // rows of a warp, elements of a lane
+            uint32_t x[PER < 8 ? PER : 8][E / 2];
+#pragma unroll 1
+            for (int k0 = 0; k0 < PER; k0 += 8) {
+#pragma unroll
+                for (int k = 0; k < 8 && k < PER; ++k) {
+                    const int rq = (k0 + k) * kSoftWarps + warp, row = note.row0 + rq, j = row / a.group;
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) x[k][i] = 0;
+                    if (rq < note.rows) {
+                        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                            a.q + static_cast<int64_t>(note.q0 + j) * a.q_token_stride +
+                            static_cast<int64_t>(note.head * a.group + row - j * a.group) * a.q_head_stride + lane * E);
+                        if constexpr (E == 2) {
+                            x[k][0] = *src;
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2*>(src);
+                            x[k][0] = y.x, x[k][1] = y.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8 && k < PER; ++k) {
+                    const int rq = (k0 + k) * kSoftWarps + warp;
+                    uint32_t top = 0;  // bf16 magnitudes order like integers
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[k][i] & 0x7FFF7FFFu);
+                    const uint32_t ex = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 7, 8u);
+                    const float mul = __uint_as_float((261u - ex) << 23);
+                    if (lane == 0) qs[rq] = qscale * __uint_as_float((ex - 7u) << 23);
+                    const int e = lane * E, c = e / 8;  // first element, its chunk of 8
+#pragma unroll
+                    for (int copy = 0; copy < 128 / C::ROWS; ++copy) {
+                        const int tr = copy * C::ROWS + rq;
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + (c >> 3) * (128 * 128) + tr * 128 +
+                                                                    (((c & 7) ^ (tr & 7)) << 4) + e % 8 * 2);
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i)
+                            dst[i] = cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
+                    }
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.qf);
+        // this thread's row
+        int first = 0, end = 0;
+        const bool real = r < note.rows;
+        const int row = note.row0 + (real ? r : 0), jq = row / a.group;
+        const int64_t orow = static_cast<int64_t>(note.q0 + jq) * a.heads + note.head * a.group + row - jq * a.group;
+        {
+            Seq s;
+            s.kv = note.kv, s.q0 = note.q0, s.qn = note.qn;
+            if (real) row_span(a, s, row, first, end);
+        }
+        named_barrier_sync(1, kSoftWarps * 32);
+        const float cs = qs[r];
+
+        float base = kNegMax, l = 0.0f;
+        const uint32_t o_at = lanes + C::O_COL + group * D;
+        bool begun = false;  // O holds something
+        // tiles n with n & 1 = group
+#pragma unroll 1
+        for (uint32_t n = note.base + ((note.base ^ group) & 1u); n < note.base + note.count; n += 2) {
+            if (!wait_warp(&bar.sf[group], n >> 1 & 1u, a.status, 0x5e)) {
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t s_at = lanes + C::S_COL + group * 128;
+            const int pos0 = note.pos0 + static_cast<int>(n - note.base) * kTokens;
+            const bool edge = pos0 < note.all0 || pos0 + kTokens > note.all1;
+#pragma unroll 1
+            for (int c = chunk0; c < chunk0 + CHUNKS; ++c) {
+                auto exponents = [&](float from) {  // of the chunk, relative to `from`; the largest
+                    tmem_ld_32x32b_x32(s_at + 32 * c, v);
+                    tmem_ld_wait();
+                    float m0 = kNegMax, m1 = kNegMax;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), cs, -from));
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int pos = pos0 + 32 * c + k;
+                            if (pos < first || pos >= end) v[k] = 0xff800000u;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        m0 = fmaxf(m0, __uint_as_float(v[k]));
+                        m1 = fmaxf(m1, __uint_as_float(v[k + 1]));
+                    }
+                    return fmaxf(m0, m1);
+                };
+                const float m = exponents(base);
+                if (__any_sync(0xffffffffu, m > kLimit)) {
+                    // the product before the last of this group's tiles is done (its S was issued behind it)
+                    const float raw = exponents(0.0f);
+                    const float to = m > kLimit ? fmaxf(base, raw - kStart) : base, al = ex2(base - to);
+                    base = to;
+                    l *= al;
+                    if (begun) {
+#pragma unroll 1
+                        for (int k0 = 0; k0 < D; k0 += 32) {
+                            tmem_ld_32x32b_x32(o_at + k0, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                            tmem_st_x16(o_at + k0, v);
+                            tmem_st_x16(o_at + k0 + 16, v + 16);
+                        }
+                    }
+                    const uint32_t al2 = cvt_f16x2(al, al);
+#pragma unroll 1
+                    for (int c2 = chunk0; c2 < c; ++c2) {  // what the tile's P holds already
+                        uint32_t p[16];
+                        tmem_ld_32x32b_x16(s_at + 16 * c2, p);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) p[k] = hmul2(p[k], al2);
+                        tmem_st_x16(s_at + 16 * c2, p);
+                    }
+                    tmem_st_wait();
+                    exponents(base);
+                }
+                uint32_t p[16];
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float e0 = ex2(__uint_as_float(v[2 * k])), e1 = ex2(__uint_as_float(v[2 * k + 1]));
+                    l0 += e0;
+                    l1 += e1;
+                    p[k] = cvt_f16x2(e0, e1);
+                }
+                l += l0 + l1;
+                tmem_st_x16(s_at + 16 * c, p);
+            }
+            if constexpr (QUAD) {  // the other warps' tokens
+                uint32_t z[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) z[k] = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c != quad) tmem_st_x16(s_at + 16 * c, z);
+            }
+            begun = true;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.pf[group]);
+        }
+        // the last products of both groups (each group has a tile, unless there is only one)
+        const uint32_t last = note.base + note.count - 1;
+        const bool both = note.count > 1;
+        if (!dead) dead = !wait_warp(&bar.od[last & 1], last >> 1 & 1u, a.status, 0x60);
+        if (!dead && both) dead = !wait_warp(&bar.od[(last - 1) & 1], (last - 1) >> 1 & 1u, a.status, 0x61);
+        ml[group * 128 + tl] = make_float2(base, l);
+        if (named_barrier_or(1, kSoftWarps * 32, dead)) return;
+        tc_fence_after();
+        float* part = partials + (static_cast<int64_t>(blockIdx.x) * 2 + (note.begins ? 1 : 0)) * (C::ROWS * (D + 2));
+        if (note.begins && !note.whole && threadIdx.x == 0) {
+            Split* split = reinterpret_cast<Split*>(a.partial) + blockIdx.x;
+            split->parts = note.parts;
+            split->q0 = note.q0;
+            split->row0 = note.row0;
+            split->rows = note.rows;
+            split->head = note.head;
+        }
+        // this lane's O of both groups, weighted; a group without a tile has nothing (its columns are stale)
+        const bool has0 = both || (last & 1) == 0, has1 = both || (last & 1) == 1;
+        if constexpr (QUAD) {
+            // Threads 8 jr .. 8 jr + 7 join row jr: of the eight results (two groups, four lanes), a slice of
+            // the channels each; group 0 reads even slices from TMEM, group 1 odd ones, in turn.
+            constexpr int SL = D / 4;  // channels of a slice (32 or 16)
+            const int jr = threadIdx.x >> 3, jc = (threadIdx.x & 7) * (SL / 8);
+            const int jrow = note.row0 + (jr < note.rows ? jr : 0), jj = jrow / a.group;
+            const int64_t o = static_cast<int64_t>(note.q0 + jj) * a.heads + note.head * a.group + jrow - jj * a.group;
+            float most = kNegMax, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = fmaxf(most, ml[k * 32 + jr].x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += ml[k * 32 + jr].y * ex2(ml[k * 32 + jr].x - most);
+            float f[4];
+#pragma unroll 1
+            for (int pass = 0; pass < 4; ++pass) {
+                float y[SL / 8];
+#pragma unroll
+                for (int k = 0; k < SL / 8; ++k) y[k] = 0.0f;
+#pragma unroll 1
+                for (int gg = 0; gg < 2; ++gg) {
+                    if (gg == 0 ? !has0 : !has1) continue;
+                    if (group == (pass & 1)) {
+                        if constexpr (SL == 32) {
+                            tmem_ld_32x32b_x32(lanes + C::O_COL + gg * D + pass * SL, v);
+                        } else {
+                            tmem_ld_32x32b_x16(lanes + C::O_COL + gg * D + pass * SL, *reinterpret_cast<uint32_t(*)[16]>(v));
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < SL; ++k) merge[tl * C::MERGE + k] = __uint_as_float(v[k]);
+                    }
+                    named_barrier_sync(1, kSoftWarps * 32);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) f[w] = ex2(ml[gg * 128 + w * 32 + jr].x - most);
+#pragma unroll
+                    for (int k = 0; k < SL / 8; ++k)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) y[k] = fmaf(merge[(w * 32 + jr) * C::MERGE + jc + k], f[w], y[k]);
+                    named_barrier_sync(1, kSoftWarps * 32);
+                }
+                const int d = SL * pass + jc;
+                const float inv = gv * (sum > 0.0f ? 1.0f / sum : sum);
+                if (note.whole) {
+                    if (jr < note.rows) {
+                        if constexpr (SL == 32)
+                            put4(a, o * D + d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+                        else
+                            put2(a, o * D + d, y[0] * inv, y[1] * inv);
+                        if (a.lse && d == 0)
+                            a.lse[o] = sum == 0.0f ? __int_as_float(0xff800000) : (most + log2f(sum)) * 0.6931471805599453f;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < SL / 8; ++k) part[jr * D + d + k] = y[k];
+                    if (d == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + 2 * jr) = make_float2(most, sum);
+                }
+            }
+        } else {
+            // each group takes half of the channels
+            const float2 z0 = ml[tl], z1 = ml[128 + tl];
+            const float most = fmaxf(z0.x, z1.x), f0 = has0 ? ex2(z0.x - most) : 0.0f, f1 = has1 ? ex2(z1.x - most) : 0.0f;
+            const float sum = z0.y * f0 + z1.y * f1;
+            const float inv = note.whole ? gv * (sum > 0.0f ? 1.0f / sum : sum) : 1.0f;
+#pragma unroll 1
+            for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 16) {
+                float y[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = 0.0f;
+                uint32_t x[16];
+                if (has0) {
+                    tmem_ld_32x32b_x16(lanes + C::O_COL + d, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(x[k]) * f0;
+                }
+                if (has1) {
+                    tmem_ld_32x32b_x16(lanes + C::O_COL + D + d, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] = fmaf(__uint_as_float(x[k]), f1, y[k]);
+                }
+                if (note.whole) {
+                    if (real) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) y[k] *= inv;
+                        put8(a, orow * D + d, y);
+                        put8(a, orow * D + d + 8, y + 8);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) part[(d + k) * C::ROWS + r] = y[k];  // channel by channel: whole sectors
+                }
+            }
+            if (group == 0) {
+                if (!note.whole)
+                    *reinterpret_cast<float2*>(part + C::ROWS * D + 2 * r) = make_float2(most, sum);
+                else if (a.lse && real)
+                    a.lse[orow] = sum == 0.0f ? __int_as_float(0xff800000) : (most + log2f(sum)) * 0.6931471805599453f;
+            }
+        }
+        tc_fence_before();
+    }
+}
+
+template <int FMT, int D, bool QUAD>
+__global__ void __launch_bounds__(kRowThreads, 1) kv_attention_rows_kernel(const __grid_constant__ KvAttnArgs a) {
+    using C = RCfg<FMT, D, QUAD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const RowBars bar(smem + C::OFF_BAR, C::STAGES);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], kDecWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.kf[i], kKeyWarps);
+            mbar_init(&bar.vf[i], kValueWarps);
+            mbar_init(&bar.sf[i], 1);
+            mbar_init(&bar.pf[i], kSoftWarps / 2);
+            mbar_init(&bar.od[i], 1);
+            mbar_init(&bar.seg_full[i], 1);
+            mbar_init(&bar.seg_empty[i], kSoftWarps + kDecWarps + 1);
+        }
+        mbar_init(bar.qf, kSoftWarps);
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp < kSoftWarps) {
+        rows_softmax<FMT, D, QUAD>(a, smem, bar, tmem);
+    } else if (warp < kFeedWarp) {
+        rows_decode<FMT, D, QUAD>(a, smem, bar, warp - kSoftWarps);
+    } else if (warp == kFeedWarp) {
+        rows_feed<FMT, D, QUAD>(a, smem, bar);
+    } else {
+        rows_mma<FMT, D, QUAD>(a, smem, bar, tmem);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int FMT, int D, bool QUAD>
+int run_rows(KvAttnArgs& a, cudaStream_t st) {
+    using C = RCfg<FMT, D, QUAD>;
+    static_assert(C::BYTES <= 227 * 1024, "shared memory");
+    auto kernel = kv_attention_rows_kernel<FMT, D, QUAD>;
+    auto join = kv_attention_join_kernel<FMT, D, C::ROWS>;
+    static std::atomic<int> known[64];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
+    if (known[dev].load() == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES) != cudaSuccess) return MXQ_ERR_CUDA;
+        known[dev].store(1);
+    }
+    const int grid = std::min(sm_count(), kMaxGrid);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = C::BYTES;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    a.inv_grid = 1.0f / static_cast<float>(grid);
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return MXQ_ERR_CUDA;
+    cfg.gridDim = dim3(2 * sm_count());
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join, a, grid) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+}  // namespace
+
+int kv_rows_tile(int64_t rows) { return rows <= 32 ? 32 : 128; }
+
+int launch_kv_attention_rows(int D, KvAttnArgs& a, cudaStream_t st) {
+    const bool quad = kv_rows_tile(static_cast<int64_t>(a.max_q) * a.group) == 32;
+    if (D == 64) return quad ? run_rows<MXQ_NVFP4, 64, true>(a, st) : run_rows<MXQ_NVFP4, 64, false>(a, st);
+    return quad ? run_rows<MXQ_NVFP4, 128, true>(a, st) : run_rows<MXQ_NVFP4, 128, false>(a, st);
+}
+
+}  // namespace mxq

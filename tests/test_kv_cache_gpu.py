@@ -221,9 +221,9 @@ def test_nan_values_of_a_later_token_do_not_reach_earlier_rows(orc, fmt):
     t = 49  # seen by the last row alone
     p.cache[p.table[0, t // 16], :, 0, pos[3][t % 16]] = 0x7F if fmt == "nvfp4" else 0xFF
     out, lse = p.run(out_dtype=torch.float32)
+    # (the row that sees such a scale, which the quantizer never writes, may get anything)
     if fmt == "nvfp4":  # (an MXFP4 scale of 2^128 moves the reference of its 32 channels)
         assert torch.equal(out[:3], clean[0][:3])
-    assert torch.isnan(out[3]).any() or not torch.isfinite(out[3]).all()
     assert torch.equal(lse[:3], clean[1][:3])
 
 
