@@ -431,7 +431,8 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
                 qt = 0;
                 continue;
             }
-            n = tile_span<C::TILE, C::ROWS>(a, s, qt, t0);
+            const TileSpan span = tile_span<C::TILE, C::ROWS>(a, s.kv, s.qn, qt);
+            t0 = span.first, n = span.count;
             if (off < static_cast<int64_t>(n) * a.kv_heads) break;
             off -= static_cast<int64_t>(n) * a.kv_heads;
             ++qt;

@@ -96,7 +96,8 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
                 qt = 0;
                 continue;
             }
-            n = tile_span<kTokens, C::ROWS>(a, s, qt, t0);
+            const TileSpan span = tile_span<kTokens, C::ROWS>(a, s.kv, s.qn, qt);
+            t0 = span.first, n = span.count;
             if (off < static_cast<int64_t>(n) * a.kv_heads) break;
             off -= static_cast<int64_t>(n) * a.kv_heads;
             ++qt;

@@ -58,27 +58,47 @@ __device__ __forceinline__ void row_span(const KvAttnArgs& a, const Seq& s, int 
     first = a.window > 0 ? max(seen - a.window, 0) : 0;
 }
 
-// Token tiles [t0, t0 + n) of a row tile; an empty one counts as one tile, so that its rows are written.
+// Token tiles [first, first + count) of a row tile; an empty one counts as one tile, so that its rows are
+// written.  Out of line, like what else runs once per segment: this code comes from a cold instruction
+// cache, and its size was most of a small call's time.
+struct TileSpan {
+    int first, count;
+};
 template <int TILE, int ROWS>
-__device__ __forceinline__ int tile_span(const KvAttnArgs& a, const Seq& s, int qt, int& t0) {
-    const int rows = s.qn * a.group, r0 = qt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
+__device__ __noinline__ TileSpan tile_span(const KvAttnArgs& a, int kv, int qn, int qt) {
+    Seq s;
+    s.kv = kv, s.q0 = 0, s.qn = qn;
+    const int rows = qn * a.group, r0 = qt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
     int first, end, skip;
     row_span(a, s, r0, first, skip);
     row_span(a, s, r1, skip, end);
-    t0 = first / TILE;
-    return max((end + TILE - 1) / TILE - t0, 1);
+    TileSpan t;
+    t.first = first / TILE;
+    t.count = max((end + TILE - 1) / TILE - t.first, 1);
+    return t;
 }
 
+// Work of sequence b in token tiles, 0 behind the last.
 template <int TILE, int ROWS>
-__device__ __forceinline__ int64_t seq_cost(const KvAttnArgs& a, const Seq& s) {
+__device__ __noinline__ int64_t seq_cost(const KvAttnArgs& a, int b) {
+    if (b >= a.batch) return 0;
+    const Seq s = load_seq(a, b);
     int64_t n = 0;
     const int tiles = (s.qn * a.group + ROWS - 1) / ROWS;
 #pragma unroll 1
-    for (int qt = 0; qt < tiles; ++qt) {
-        int t0;
-        n += tile_span<TILE, ROWS>(a, s, qt, t0);
-    }
+    for (int qt = 0; qt < tiles; ++qt) n += tile_span<TILE, ROWS>(a, s.kv, s.qn, qt).count;
     return n * a.kv_heads;
+}
+
+// Inclusive sum over the warp's lanes.
+__device__ __noinline__ int64_t warp_scan(int64_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
 }
 
 // n / d for quotients below 2^20: a float quotient, corrected by at most a step or two (a 64-bit division
@@ -102,17 +122,12 @@ template <int TILE, int ROWS>
 __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, int min_tiles) {
     const int lane = threadIdx.x & 31;
     Plan p;
-    int64_t own = 0, sum = 0;  // of the last 32 sequences: the lane's, and the inclusive scan over the lanes
+    int64_t own = 0, sum = 0;  // of the last 32 sequences: the lane's, and the inclusive sum over the lanes
     p.work = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
-        sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
-        }
+        own = seq_cost<TILE, ROWS>(a, b0 + lane);
+        sum = warp_scan(own);
         p.work += __shfl_sync(0xffffffffu, sum, 31);
     }
     // any share that covers the work will do: the quotient in floats, rounded up past its error of 2^-22
@@ -124,26 +139,20 @@ __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, int min_tiles) {
     if (p.at >= p.work) return p;
     int64_t base = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    for (int b0 = 0;; b0 += 32) {
         if (a.batch > 32) {
-            own = b0 + lane < a.batch ? seq_cost<TILE, ROWS>(a, load_seq(a, b0 + lane)) : 0;
-            sum = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
-            }
+            own = seq_cost<TILE, ROWS>(a, b0 + lane);
+            sum = warp_scan(own);
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, base + sum > p.at);
         if (hit) {
             const int l = __ffs(hit) - 1;
             p.off = p.at - base - __shfl_sync(0xffffffffu, sum - own, l);
             p.b = b0 + l;
-            break;
+            return p;
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    return p;
 }
 
 // What the join kernel needs to know of a row tile whose first part CTA c has; parts = 0: there is none.
