@@ -54,8 +54,11 @@ struct Cfg {
     static constexpr int BUDGET = (227 / CTAS - 1) * 1024 - 1024;
     static constexpr int FIXED = 2 * Q_BYTES + RED + 2 * (ROWS * 12 + 64) + kWarps * ROWS * 8 + 64;
     static constexpr int FIT = (BUDGET - FIXED) / (TILE_BYTES + 16);
-    static constexpr int STAGES = FIT < 16 ? FIT : 16;
-    static_assert(STAGES >= kWarps, "shared memory");
+    // A multiple of kWarps: tile n goes to warp n % kWarps, so that a slot's uses are all of one warp, in turn.
+    // (Were they not, a warp could wait for use c of a slot whose use c - 1, another warp's, has not landed: the
+    // barrier's one parity bit would let it pass.)
+    static constexpr int STAGES = (FIT < 16 ? FIT : 16) / kWarps * kWarps;
+    static_assert(STAGES >= 2 * kWarps, "shared memory");
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = STAGES * TILE_BYTES;
     static constexpr int OFF_RED = OFF_Q + 2 * Q_BYTES;
@@ -445,22 +448,25 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
         row_span(a, s, row0, seen0, all1);
         row_span(a, s, row0 + rows - 1, all0, seen1);
 
-        // lane i holds the place of the i-th unit ahead: byte offset, -1 for one that is not loaded
-        const int first_unit = (t0 + from) * C::TU, end_unit = first_unit + count * C::TU;
-        const int units_end = min((seen1 + 15) >> 4, end_unit);  // behind the tokens pages may not exist
-        auto source_of = [&](int i) -> int64_t {
-            const int unit = first_unit + i + lane;
-            if (unit >= units_end) return -1;
-            const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));  // unit / page_units
-            const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
-            if (pg < 0 || pg >= a.num_pages) {
-                kv_status(a.status, kStatusKvPage);
-                return -1;
+        // A lane has every BATCH-th token tile: it finds the tile's units (byte offsets, -1: not loaded) one
+        // batch ahead and starts the copies itself when their ring slot is free.  (One elected lane that did all
+        // of it took 600 cycles a tile, three times what HBM takes to deliver one.)
+        constexpr int BATCH = 8;
+        static_assert(BATCH <= C::STAGES, "a slot comes up once in a batch: its barrier has one parity bit");
+        const int first_unit = (t0 + from) * C::TU;
+        const int units_end = min((seen1 + 15) >> 4, first_unit + count * C::TU);  // behind the tokens pages may not exist
+        int page[C::TU], in_page[C::TU];  // of the lane's units of the next batch; page is not looked at before it is used
+        auto look_up = [&](int tile) {    // for the batch that begins at `tile`
+#pragma unroll
+            for (int u = 0; u < C::TU; ++u) {
+                const int unit = first_unit + (tile + lane) * C::TU + u;
+                const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));  // unit / page_units
+                in_page[u] = lane < BATCH && unit < units_end ? unit - at_page * a.page_units : -1;
+                page[u] = 0;
+                if (in_page[u] >= 0) page[u] = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             }
-            return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
-                   static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
         };
-        int64_t source = -1, source_next = source_of(0);
+        look_up(0);
         // Q rows in flight beside them: lane (g, t) takes what it needs of row g as the B operand of S, 8
         // elements (two k steps) a load, as the K codes are dealt to the lanes
         constexpr int LOADS = D / 32;
@@ -491,36 +497,53 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
         }
         // The first segment's copies start in front of its note (the ring is empty); later ones behind it,
         // as their slots come free only while the computing warps are at the segment before.
-        int issued = 0, limit = nseg == 0 ? min(count, C::STAGES) : 0;
+        int issued = 0, limit = nseg == 0 ? min(count, C::STAGES / BATCH * BATCH) : 0;
 #pragma unroll 1
         for (int phase = 0; phase < 2; ++phase, limit = count) {
 #pragma unroll 1
-            for (; issued < limit; ++issued, ++tiles) {
-                const int i = issued * C::TU % 32;
-                if (i == 0) {
-                    source = source_next;
-                    source_next = source_of(issued * C::TU + 32);
-                }
-                const uint32_t slot = tiles % C::STAGES;
-                if (!wait_warp(&empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x42)) return;
+            for (; issued < limit; issued += BATCH) {
                 int64_t src[C::TU];
 #pragma unroll
-                for (int u = 0; u < C::TU; ++u) src[u] = __shfl_sync(0xffffffffu, source, i + u);
-                if (elect_one()) {
-                    uint8_t* dst = smem + C::OFF_RING + slot * C::TILE_BYTES;
-                    uint32_t bytes = 0;
+                for (int u = 0; u < C::TU; ++u) {
+                    src[u] = -1;
+                    if (in_page[u] < 0) continue;
+                    if (page[u] < 0 || page[u] >= a.num_pages) {
+                        kv_status(a.status, kStatusKvPage);
+                        continue;
+                    }
+                    src[u] = (static_cast<int64_t>(page[u]) * a.kv_heads + head) * a.page_bytes +
+                             static_cast<int64_t>(in_page[u]) * U::BYTES;
+                }
+                look_up(issued + BATCH);
+                const uint32_t n = tiles + issued + lane, slot = n % C::STAGES, parity = (n / C::STAGES & 1u) ^ 1u;
+                bool todo = lane < BATCH && issued + lane < count;
+                uint64_t since = 0;
+#pragma unroll 1
+                for (uint32_t polls = 0; __any_sync(0xffffffffu, todo); ++polls) {
+                    if (todo && mbar_test_wait(&empty[slot], parity)) {
+                        todo = false;
+                        uint8_t* dst = smem + C::OFF_RING + slot * C::TILE_BYTES;
+                        uint32_t bytes = 0;
 #pragma unroll
-                    for (int u = 0; u < C::TU; ++u) bytes += src[u] < 0 ? 0 : U::BYTES;
-                    mbar_arrive_expect_tx(&full[slot], bytes);
-                    if (C::TU == 2 && src[0] >= 0 && src[C::TU - 1] == src[0] + U::BYTES) {  // neighbours in one page
-                        bulk_load(dst, a.cache + src[0], 2 * U::BYTES, &full[slot]);
-                    } else {
+                        for (int u = 0; u < C::TU; ++u) bytes += src[u] < 0 ? 0 : U::BYTES;
+                        mbar_arrive_expect_tx(&full[slot], bytes);
+                        if (C::TU == 2 && src[0] >= 0 && src[C::TU - 1] == src[0] + U::BYTES) {  // neighbours in one page
+                            bulk_load(dst, a.cache + src[0], 2 * U::BYTES, &full[slot]);
+                        } else {
 #pragma unroll
-                        for (int u = 0; u < C::TU; ++u)
-                            if (src[u] >= 0) bulk_load(dst + u * U::BYTES, a.cache + src[u], U::BYTES, &full[slot]);
+                            for (int u = 0; u < C::TU; ++u)
+                                if (src[u] >= 0) bulk_load(dst + u * U::BYTES, a.cache + src[u], U::BYTES, &full[slot]);
+                        }
+                    }
+                    __syncwarp();
+                    if ((polls & 255u) == 255u) {  // (a bounded wait, as all others)
+                        if (since == 0) since = globaltimer();
+                        if (__any_sync(0xffffffffu, globaltimer() - since > kWaitLimitNs)) {
+                            if (lane == 0) atomicCAS(a.status, 0, kStatusTimeoutBase + 0x42);
+                            return;
+                        }
                     }
                 }
-                __syncwarp();
             }
             if (phase == 1) break;
             // Q operands: rows as f16 times a power of two
@@ -562,6 +585,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_full[buf]);
         }
+        tiles += count;
         at += count;
         off += count;
     }
@@ -622,9 +646,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 
         Warp<FMT, D, NT> w;
         warp_reset(w);
-        int pos0 = seg.pos0 + warp * C::TILE;
+        // tile i of the segment is tile base + i of the CTA, which warp (base + i) % kWarps takes
+        int first = warp - static_cast<int>(base % kWarps);
+        if (first < 0) first += kWarps;
+        int pos0 = seg.pos0 + first * C::TILE;
 #pragma unroll 1
-        for (int i = warp; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
+        for (int i = first; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
             const uint32_t slot = (base + i) % C::STAGES;
             if (!wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
                 dead = true;
