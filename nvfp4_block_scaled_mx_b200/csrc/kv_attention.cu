@@ -407,8 +407,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
     int b = plan.b, qt = 0;
-    Seq s = {};
-    if (at < stop) s = load_seq(a, b);
+    Seq s = plan.s;
     float qscale = a.scale * 1.4426950408889634f;
     if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k;
     uint32_t tiles = 0, nseg = 0;

@@ -80,8 +80,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
     int b = plan.b, qt = 0;
-    Seq s = {};
-    if (at < stop) s = load_seq(a, b);
+    Seq s = plan.s;
     uint32_t tiles = 0;
 #pragma unroll 1
     for (uint32_t nseg = 0;; ++nseg) {

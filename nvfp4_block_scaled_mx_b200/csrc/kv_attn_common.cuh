@@ -29,25 +29,16 @@ struct Seq {
 };
 
 __device__ __noinline__ Seq load_seq(const KvAttnArgs& a, int b) {
+    // all loads first: one round trip
+    const bool given = a.q_start != nullptr;
+    const int kv = a.lens[b], q0 = given ? a.q_start[b] : b * a.max_q, q1 = given ? a.q_start[b + 1] : q0 + a.max_q;
     Seq s;
-    s.kv = a.lens[b];
-    if (s.kv > a.max_len) {
-        kv_status(a.status, kStatusKvLen);
-        s.kv = a.max_len;
-    }
-    s.kv = max(s.kv, 0);
-    if (a.q_start) {
-        const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
-        s.q0 = q0;
-        s.qn = max(q1 - q0, 0);
-        if (q0 < 0 || q1 > a.rows_total || s.qn > a.max_q) {
-            kv_status(a.status, kStatusKvRows);
-            s.q0 = s.qn = 0;
-        }
-    } else {
-        s.q0 = b * a.max_q;
-        s.qn = a.max_q;
-    }
+    s.kv = min(max(kv, 0), a.max_len);
+    s.q0 = q0;
+    s.qn = max(q1 - q0, 0);
+    const bool bad_rows = q0 < 0 || q1 > a.rows_total || s.qn > a.max_q;
+    if (bad_rows) s.q0 = s.qn = 0;
+    if (bad_rows || kv > a.max_len) kv_status(a.status, bad_rows ? kStatusKvRows : kStatusKvLen);
     return s;
 }
 
@@ -70,23 +61,21 @@ __device__ __noinline__ TileSpan tile_span(const KvAttnArgs& a, int kv, int qn, 
     s.kv = kv, s.q0 = 0, s.qn = qn;
     const int rows = qn * a.group, r0 = qt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
     int first, end, skip;
-    row_span(a, s, r0, first, skip);
-    row_span(a, s, r1, skip, end);
+    row_span(a, s, r0, first, end);
+    if (a.max_q > 1) row_span(a, s, r1, skip, end);  // (the rows of one query token see the same)
     TileSpan t;
     t.first = first / TILE;
     t.count = max((end + TILE - 1) / TILE - t.first, 1);
     return t;
 }
 
-// Work of sequence b in token tiles, 0 behind the last.
+// Work of a sequence in token tiles.
 template <int TILE, int ROWS>
-__device__ __noinline__ int64_t seq_cost(const KvAttnArgs& a, int b) {
-    if (b >= a.batch) return 0;
-    const Seq s = load_seq(a, b);
+__device__ __noinline__ int64_t seq_cost(const KvAttnArgs& a, int kv, int qn) {
     int64_t n = 0;
-    const int tiles = (s.qn * a.group + ROWS - 1) / ROWS;
+    const int tiles = (qn * a.group + ROWS - 1) / ROWS;
 #pragma unroll 1
-    for (int qt = 0; qt < tiles; ++qt) n += tile_span<TILE, ROWS>(a, s.kv, s.qn, qt).count;
+    for (int qt = 0; qt < tiles; ++qt) n += tile_span<TILE, ROWS>(a, kv, qn, qt).count;
     return n * a.kv_heads;
 }
 
@@ -116,42 +105,61 @@ __device__ __forceinline__ int div_small(int64_t n, int64_t d, int64_t& r) {
 struct Plan {
     int64_t work, per, at, off;
     int b;
+    Seq s;  // sequence b
 };
 
 template <int TILE, int ROWS>
 __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, int min_tiles) {
     const int lane = threadIdx.x & 31;
     Plan p;
-    int64_t own = 0, sum = 0;  // of the last 32 sequences: the lane's, and the inclusive sum over the lanes
+    // of the last 32 sequences: the lane's, its work, and the inclusive sum over the lanes
+    Seq s = {};
+    int64_t own = 0, sum = 0;
     p.work = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        own = seq_cost<TILE, ROWS>(a, b0 + lane);
-        sum = warp_scan(own);
-        p.work += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    // any share that covers the work will do: the quotient in floats, rounded up past its error of 2^-22
-    p.per = static_cast<int64_t>(static_cast<float>(p.work) * a.inv_grid * 1.000001f) + 1;
-    if (p.per < min_tiles) p.per = min_tiles;
-    p.at = p.per * blockIdx.x;
-    p.b = a.batch;
-    p.off = 0;
-    if (p.at >= p.work) return p;
+    p.at = 0;
+    p.s = s;
+    bool locate = false;
     int64_t base = 0;
 #pragma unroll 1
-    for (int b0 = 0;; b0 += 32) {
-        if (a.batch > 32) {
-            own = seq_cost<TILE, ROWS>(a, b0 + lane);
+    for (int b0 = 0;; b0 += 32) {  // once for the sum, and again (for more than 32 sequences) to find the place
+        if (b0 >= a.batch) {
+            if (locate) return p;  // (never: the place lies in front of the end)
+            // any share that covers the work will do: the quotient in floats, rounded up past its error of 2^-22
+            p.per = static_cast<int64_t>(static_cast<float>(p.work) * a.inv_grid * 1.000001f) + 1;
+            if (p.per < min_tiles) p.per = min_tiles;
+            p.at = p.per * blockIdx.x;
+            p.b = a.batch;
+            p.off = 0;
+            if (p.at >= p.work) return p;
+            locate = true;
+            b0 = a.batch > 32 ? 0 : b0 - 32;
+        }
+        if (!locate || a.batch > 32) {
+            s = {};
+            own = 0;
+            if (b0 + lane < a.batch) {
+                s = load_seq(a, b0 + lane);
+                own = seq_cost<TILE, ROWS>(a, s.kv, s.qn);
+            }
+            __syncwarp();
             sum = warp_scan(own);
+        }
+        const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
+        if (!locate) {
+            p.work += all;
+            continue;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, base + sum > p.at);
         if (hit) {
             const int l = __ffs(hit) - 1;
             p.off = p.at - base - __shfl_sync(0xffffffffu, sum - own, l);
             p.b = b0 + l;
+            p.s.kv = __shfl_sync(0xffffffffu, s.kv, l);
+            p.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+            p.s.qn = __shfl_sync(0xffffffffu, s.qn, l);
             return p;
         }
-        base += __shfl_sync(0xffffffffu, sum, 31);
+        base += all;
     }
 }
 
@@ -313,9 +321,14 @@ __device__ __forceinline__ void join_add(float& m, float& l, float4& v, float m2
 
 template <int FMT, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const __grid_constant__ KvAttnArgs a, int grid) {
+    // a row tile of few parts is one item of all channels; of more, SLICES items
     constexpr int SLICE = ROWS > 64 ? 8 : 16, SLICES = D / SLICE, ELEMS = ROWS * SLICE / 4, PG = kJoinThreads / ELEMS, BATCH = 8;
-    __shared__ uint32_t has[kMaxGrid / 32];
-    __shared__ int list[kMaxGrid], count;
+    constexpr int FEW = ROWS > 64 ? 0 : 4;
+    // Parts of 128 rows lie channel by channel (their threads had a row each), smaller ones row by row.
+    constexpr bool TRANSPOSED = ROWS == 128;
+    constexpr int PART = ROWS * (D + 2);
+    __shared__ uint32_t has[2][kMaxGrid / 32];
+    __shared__ int list[2][kMaxGrid], count[2];  // [0] of few parts, [1] of more
     __shared__ float2 mls[PG][ELEMS];
     __shared__ float4 vs[PG][ELEMS];
     pdl_launch_dependents();
@@ -323,57 +336,51 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const _
     const Split* splits = reinterpret_cast<const Split*>(a.partial);
     const float* partials = a.partial + grid * (sizeof(Split) / 4);
     const float gv = FMT == MXQ_NVFP4 ? *a.g_v : 1.0f;
-    // the list is the same in every block: CTAs in order, placed by counting those in front
-    uint32_t mask[kMaxGrid / kJoinThreads];
+    // the lists are the same in every block: CTAs in order, placed by counting those in front
+    int parts[kMaxGrid / kJoinThreads];
 #pragma unroll
     for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
         const int c = i * kJoinThreads + threadIdx.x;
-        mask[i] = c < grid ? splits[c].parts : 0;
+        parts[i] = c < grid ? splits[c].parts : 0;
     }
 #pragma unroll
     for (int i = 0; i < kMaxGrid / kJoinThreads; ++i) {
-        const uint32_t m = __ballot_sync(0xffffffffu, mask[i] != 0);
-        if ((threadIdx.x & 31) == 0) has[(i * kJoinThreads + threadIdx.x) / 32] = m;
+        const uint32_t m = __ballot_sync(0xffffffffu, parts[i] != 0 && parts[i] <= FEW);
+        const uint32_t n = __ballot_sync(0xffffffffu, parts[i] > FEW);
+        if ((threadIdx.x & 31) == 0) {
+            has[0][(i * kJoinThreads + threadIdx.x) / 32] = m;
+            has[1][(i * kJoinThreads + threadIdx.x) / 32] = n;
+        }
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
+    if (threadIdx.x < 64) {
         static_assert(kMaxGrid == 32 * 32, "one word of the mask a lane");
-        uint32_t m = has[threadIdx.x];
+        const int which = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        uint32_t m = has[which][lane];
         int before = __popc(m);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, before, o);
-            if (static_cast<int>(threadIdx.x) >= o) before += x;
+            if (lane >= o) before += x;
         }
-        if (threadIdx.x == 31) count = before;
+        if (lane == 31) count[which] = before;
         before -= __popc(m);
-        for (; m; m &= m - 1) list[before++] = threadIdx.x * 32 + __ffs(m) - 1;
+        for (; m; m &= m - 1) list[which][before++] = lane * 32 + __ffs(m) - 1;
     }
     __syncthreads();
-    constexpr int PART = ROWS * (D + 2);
-    // Parts of 128 rows lie channel by channel (their threads had a row each), smaller ones row by row.
-    constexpr bool TRANSPOSED = ROWS == 128;
-    const int pg = threadIdx.x / ELEMS, e = threadIdx.x % ELEMS;
-    const int r = TRANSPOSED ? e % ROWS : e / (SLICE / 4), e4 = TRANSPOSED ? e / ROWS : e % (SLICE / 4);
+    // four channels of row r of all parts k = from, from + step, ...
+    auto gather = [&](const float* first, int count, int r, int d, int from, int step, float& m, float& l, float4& v) {
 #pragma unroll 1
-    for (int i = blockIdx.x; i < count * SLICES; i += gridDim.x) {
-        const int c = list[i / SLICES], d = i % SLICES * SLICE + e4 * 4;
-        const Split s = splits[c];
-        // slot 1 of the first CTA, slot 0 of the others
-        const float* first = partials + (static_cast<int64_t>(c) * 2 + 1) * PART;
-        float m = kNegMax, l = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-        for (int k0 = pg < PG ? pg : s.parts; k0 < s.parts; k0 += PG * BATCH) {
+        for (int k0 = from; k0 < count; k0 += step * BATCH) {
             float2 z[BATCH];
             float4 x[BATCH];
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
-                const int k = k0 + j * PG;
+                const int k = k0 + j * step;
                 const float* at = first + (k == 0 ? 0 : (2 * k - 1) * static_cast<int64_t>(PART));
                 z[j] = make_float2(kNegMax, 0.0f);
                 x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (k < s.parts) {
+                if (k < count) {
                     z[j] = *reinterpret_cast<const float2*>(at + ROWS * D + 2 * r);
                     if constexpr (TRANSPOSED)
                         x[j] = make_float4(at[d * ROWS + r], at[(d + 1) * ROWS + r], at[(d + 2) * ROWS + r], at[(d + 3) * ROWS + r]);
@@ -384,7 +391,53 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const _
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) join_add(m, l, v, z[j].x, z[j].y, x[j]);
         }
-        if (pg < PG) {  // (ELEMS need not divide the threads)
+    };
+    auto store = [&](const Split& s, int r, int d, float m, float l, const float4& v) {
+        const int row = s.row0 + r, j = a.max_q == 1 ? 0 : row / a.group;
+        const int64_t o = static_cast<int64_t>(s.q0 + j) * a.heads + s.head * a.group + row - j * a.group;
+        const float inv = gv * (l > 0.0f ? 1.0f / l : l);  // l is 0 (no token) or not a number
+        put4(a, o * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        if (a.lse && d == 0) a.lse[o] = l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
+    };
+#pragma unroll 1
+    for (int i = blockIdx.x; i < count[0]; i += gridDim.x) {
+        const int c = list[0][i];
+        const Split s = splits[c];
+        // slot 1 of the first CTA, slot 0 of the others
+        const float* first = partials + (static_cast<int64_t>(c) * 2 + 1) * PART;
+#pragma unroll 1
+        for (int e = threadIdx.x; e < ROWS * D / 4; e += kJoinThreads) {
+            const int r = TRANSPOSED ? e % ROWS : e / (D / 4), d = (TRANSPOSED ? e / ROWS : e % (D / 4)) * 4;
+            if (r >= s.rows) continue;
+            float m = kNegMax, l = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < (FEW > 0 ? FEW : 1); ++k) {
+                const float* at = first + (k == 0 ? 0 : (2 * k - 1) * static_cast<int64_t>(PART));
+                if (k < s.parts) {
+                    const float2 z = *reinterpret_cast<const float2*>(at + ROWS * D + 2 * r);
+                    float4 x;
+                    if constexpr (TRANSPOSED)
+                        x = make_float4(at[d * ROWS + r], at[(d + 1) * ROWS + r], at[(d + 2) * ROWS + r], at[(d + 3) * ROWS + r]);
+                    else
+                        x = *reinterpret_cast<const float4*>(at + r * D + d);
+                    join_add(m, l, v, z.x, z.y, x);
+                }
+            }
+            store(s, r, d, m, l, v);
+        }
+    }
+    const int pg = threadIdx.x / ELEMS, e = threadIdx.x % ELEMS;
+    const int r = TRANSPOSED ? e % ROWS : e / (SLICE / 4), e4 = TRANSPOSED ? e / ROWS : e % (SLICE / 4);
+#pragma unroll 1
+    for (int i = blockIdx.x; i < count[1] * SLICES; i += gridDim.x) {
+        const int c = list[1][i / SLICES], d = i % SLICES * SLICE + e4 * 4;
+        const Split s = splits[c];
+        const float* first = partials + (static_cast<int64_t>(c) * 2 + 1) * PART;
+        float m = kNegMax, l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (pg < PG) gather(first, s.parts, r, d, pg, PG, m, l, v);  // (ELEMS need not divide the threads)
+        if (pg < PG) {
             mls[pg][e] = make_float2(m, l);
             vs[pg][e] = v;
         }
@@ -392,12 +445,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const _
         if (pg == 0 && r < s.rows) {
 #pragma unroll
             for (int k = 1; k < PG; ++k) join_add(m, l, v, mls[k][e].x, mls[k][e].y, vs[k][e]);
-            const int row = s.row0 + r;
-            const int64_t o = static_cast<int64_t>(s.q0 + row / a.group) * a.heads + s.head * a.group + row % a.group;
-            const float inv = gv * (l > 0.0f ? 1.0f / l : l);  // l is 0 (no token) or not a number
-            put4(a, o * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            if (a.lse && d == 0)
-                a.lse[o] = l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
+            store(s, r, d, m, l, v);
         }
         __syncthreads();
     }
