@@ -37,6 +37,10 @@ constexpr int kThreads = (kWarps + 1) * 32;
 #define C_MINT 4
 #endif
 constexpr int kMinTiles = C_MINT;  // token tiles a CTA gets at least
+#ifndef C_EX
+#define C_EX 10
+#endif
+constexpr int kExtraTiles = C_EX;  // counted for beginning a row tile
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -402,7 +406,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     uint64_t* seg_full = empty + C::STAGES;
     uint64_t* seg_empty = seg_full + 2;
 
-    const Plan plan = make_plan<C::TILE, C::ROWS>(a, kMinTiles);
+    const Plan plan = make_plan<C::TILE, C::ROWS, kExtraTiles>(a, kMinTiles);
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
@@ -416,18 +420,11 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     for (;; ++nseg) {
         const uint32_t buf = nseg & 1u;
         Segment* note = reinterpret_cast<Segment*>(smem + C::OFF_SEG + buf * 64);
-        if (at >= stop) {
-            if (!wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
-            if (lane == 0) {
-                note->count = -1;
-                mbar_arrive(&seg_full[buf]);
-            }
-            return;
-        }
-        // the row tile and kv head that hold work item `at`
-        int t0, n;
+        // the row tile and kv head that hold work item `at`: its token tiles [from, from + count) of n
+        int t0 = 0, n = 0, head = 0, from = 0, count = 0;
+        int64_t place = 0, share = 0;  // of the work counted for it
 #pragma unroll 1
-        for (;;) {
+        while (at < stop) {
             if (qt * C::ROWS >= s.qn * a.group) {
                 s = load_seq(a, ++b);
                 qt = 0;
@@ -435,13 +432,28 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             }
             const TileSpan span = tile_span<C::TILE, C::ROWS>(a, s.kv, s.qn, qt);
             t0 = span.first, n = span.count;
-            if (off < static_cast<int64_t>(n) * a.kv_heads) break;
-            off -= static_cast<int64_t>(n) * a.kv_heads;
-            ++qt;
+            const int64_t each = n + kExtraTiles;  // of a head
+            if (off >= each * a.kv_heads) {
+                off -= each * a.kv_heads;
+                ++qt;
+                continue;
+            }
+            head = div_small(off, each, place);
+            share = min(each - place, stop - at);
+            from = max(static_cast<int>(place) - kExtraTiles, 0);
+            count = max(static_cast<int>(place + share) - kExtraTiles, 0) - from;
+            if (count > 0) break;
+            at += share;  // nothing but tiles that are only counted
+            off += share;
         }
-        int64_t from64;
-        const int head = div_small(off, n, from64), from = static_cast<int>(from64);
-        const int count = static_cast<int>(min(static_cast<int64_t>(n - from), stop - at));
+        if (count == 0) {
+            if (!wait_warp(&seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x41)) return;
+            if (lane == 0) {
+                note->count = -1;
+                mbar_arrive(&seg_full[buf]);
+            }
+            return;
+        }
         const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.qn * a.group - row0);
         int seen0, seen1, all0, all1;
         row_span(a, s, row0, seen0, all1);
@@ -492,7 +504,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             note->begins = from == 0;
             note->whole = from == 0 && count == n;
             int64_t rest;
-            note->parts = from == 0 ? div_small(at + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
+            note->parts = from == 0 ? div_small(at - place + kExtraTiles + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
         }
         // The first segment's copies start in front of its note (the ring is empty); later ones behind it,
         // as their slots come free only while the computing warps are at the segment before.
@@ -585,8 +597,8 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
             if (lane == 0) mbar_arrive(&seg_full[buf]);
         }
         tiles += count;
-        at += count;
-        off += count;
+        at += share;
+        off += share;
     }
 }
 

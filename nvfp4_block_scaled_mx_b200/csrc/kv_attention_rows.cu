@@ -31,6 +31,10 @@ constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
 constexpr int kRowThreads = (kMmaWarp + 1) * 32;
 constexpr int kTokens = 128;  // of a tile
 constexpr int kMinRowTiles = 2;
+#ifndef C_EXR
+#define C_EXR 8
+#endif
+constexpr int kExtraRowTiles = C_EXR;  // counted for beginning a row tile
 constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^7; above 2^15 it is raised
 
 template <int FMT, int D, bool QUAD>
@@ -75,7 +79,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
     using C = RCfg<FMT, D, QUAD>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31;
-    const Plan plan = make_plan<kTokens, C::ROWS>(a, kMinRowTiles);
+    const Plan plan = make_plan<kTokens, C::ROWS, kExtraRowTiles>(a, kMinRowTiles);
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
@@ -86,10 +90,11 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
     for (uint32_t nseg = 0;; ++nseg) {
         const uint32_t buf = nseg & 1u;
         Segment* note = reinterpret_cast<Segment*>(smem + C::OFF_SEG + buf * 64);
-        const bool more = at < stop;
-        int t0 = 0, n = 1;
+        // the row tile and kv head that hold work item `at`: its token tiles [from, from + count) of n
+        int t0 = 0, n = 0, head = 0, from = 0, count = 0;
+        int64_t place = 0, share = 0;  // of the work counted for it
 #pragma unroll 1
-        while (more) {
+        while (at < stop) {
             if (qt * C::ROWS >= s.qn * a.group) {
                 s = load_seq(a, ++b);
                 qt = 0;
@@ -97,21 +102,28 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             }
             const TileSpan span = tile_span<kTokens, C::ROWS>(a, s.kv, s.qn, qt);
             t0 = span.first, n = span.count;
-            if (off < static_cast<int64_t>(n) * a.kv_heads) break;
-            off -= static_cast<int64_t>(n) * a.kv_heads;
-            ++qt;
+            const int64_t each = n + kExtraRowTiles;  // of a head
+            if (off >= each * a.kv_heads) {
+                off -= each * a.kv_heads;
+                ++qt;
+                continue;
+            }
+            head = div_small(off, each, place);
+            share = min(each - place, stop - at);
+            from = max(static_cast<int>(place) - kExtraRowTiles, 0);
+            count = max(static_cast<int>(place + share) - kExtraRowTiles, 0) - from;
+            if (count > 0) break;
+            at += share;  // nothing but tiles that are only counted
+            off += share;
         }
         if (!wait_warp(&bar.seg_empty[buf], (nseg >> 1 & 1u) ^ 1u, a.status, 0x51)) return;
-        if (!more) {
+        if (count == 0) {
             if (lane == 0) {
                 note->count = -1;
                 mbar_arrive(&bar.seg_full[buf]);
             }
             return;
         }
-        int64_t from64;
-        const int head = div_small(off, n, from64), from = static_cast<int>(from64);
-        const int count = static_cast<int>(min(static_cast<int64_t>(n - from), stop - at));
         const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.qn * a.group - row0);
         int seen0, seen1, all0, all1;
         row_span(a, s, row0, seen0, all1);
@@ -126,7 +138,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             note->begins = from == 0;
             note->whole = from == 0 && count == n;
             int64_t rest;
-            note->parts = from == 0 ? div_small(at + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
+            note->parts = from == 0 ? div_small(at - place + kExtraRowTiles + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
             mbar_arrive(&bar.seg_full[buf]);
         }
         const int first_unit = (t0 + from) * C::UNITS;
@@ -162,8 +174,8 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             }
             __syncwarp();
         }
-        at += count;
-        off += count;
+        at += share;
+        off += share;
     }
 }
 
@@ -285,19 +297,22 @@ __device__ __forceinline__ void values(uint32_t raw, uint32_t v16, int u, bool e
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t chunk = (u & 3) * 2 + h;  // of 8 tokens in the block of 64
-        const uint32_t at0 = to + ((chunk ^ (2 * g & 7)) << 4), at1 = to + 128 + ((chunk ^ ((2 * g + 1) & 7)) << 4);
+        // lanes with g >= 4 take the odd channel first: else rows 2 g and 2 (g + 4) would meet the same banks
+        const uint32_t even = to + ((chunk ^ (2 * g & 7)) << 4), odd = to + 128 + ((chunk ^ ((2 * g + 1) & 7)) << 4);
+        const uint32_t at0 = g < 4 ? even : odd, at1 = g < 4 ? odd : even;
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
             const uint32_t x = w[h][wd], y = w[h][D / 64 + wd];
-            uint32_t lo[4], hi[4];
-            e2m1x8((x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), lo);
-            e2m1x8((x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), hi);
+            const uint32_t lo = (x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), hi = (x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+            uint32_t v0[4], v1[4];
+            e2m1x8(g < 4 ? lo : hi, v0);
+            e2m1x8(g < 4 ? hi : lo, v1);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int j = 4 * wd + k;
                 const uint32_t f = e4m3x2_f16x2(j & 1 ? sb[h][j >> 1] >> 16 : sb[h][j >> 1] & 0xFFFFu);
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(hmul2(lo[k], f)) : "memory");
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(hmul2(hi[k], f)) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(hmul2(v0[k], f)) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(hmul2(v1[k], f)) : "memory");
             }
         }
     }
