@@ -8,6 +8,8 @@
 // do not depend on timing.  Page contents move in a second kernel that reads the list of copies.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "kv.cuh"
 #include "kv_internal.h"
 #include "mxq_internal.h"
@@ -27,13 +29,18 @@ constexpr int kNoPages = -3;    // fewer free pages than the call needs
 
 struct Shared {
     uint32_t seen[MXQ_KV_MAX_TABLE / 32];  // rows named by the call
-    uint32_t cow[MXQ_KV_MAX_SEQS / 32];    // reserve: sequences whose tail page is copied
-    int need[MXQ_KV_MAX_SEQS + 1];         // reserve: pages needed by the sequences in front
-    int add[MXQ_KV_MAX_SEQS + 1];          // reserve: tokens of the sequences in front
     int64_t warp_sums[32];
-    int64_t total;                         // this CTA's total, read by the others
+    int64_t total[2];                      // this CTA's total of each scan over the cluster, read by the others
+    int64_t totals[kCluster];
     int verdict;
 };
+
+struct Reserve : Shared {
+    int need[MXQ_KV_MAX_SEQS + 1];     // pages needed by the sequences in front
+    int add[MXQ_KV_MAX_SEQS + 1];      // tokens of the sequences in front
+    uint16_t copy[MXQ_KV_MAX_SEQS];    // number of the sequence's tail page among those copied, kNoCopy
+};
+constexpr uint16_t kNoCopy = 0xFFFFu;
 
 __device__ __forceinline__ int pages_for(int64_t len, int page_size) {
     return static_cast<int>((len + page_size - 1) / page_size);
@@ -62,20 +69,23 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, Shared& sh, int64_t& al
     return before + x - v;
 }
 
-// The same over the cluster, CTAs in rank order.
-__device__ __forceinline__ int64_t cluster_scan(int64_t v, Shared& sh, int64_t& all) {
+// The same over the cluster, CTAs in rank order; `slot` 0 or 1, another for each scan of a kernel.  A cluster
+// barrier has to follow before a CTA leaves: others read its total.
+__device__ __forceinline__ int64_t cluster_scan(int64_t v, Shared& sh, int slot, int64_t& all) {
     cg::cluster_group cl = cg::this_cluster();
     int64_t mine;
     const int64_t x = block_scan(v, sh, mine);
-    if (threadIdx.x == 0) sh.total = mine;
+    if (threadIdx.x == 0) sh.total[slot] = mine;
     cl.sync();
+    if (threadIdx.x < kCluster) sh.totals[threadIdx.x] = *cl.map_shared_rank(&sh.total[slot], threadIdx.x);
+    __syncthreads();
     int64_t before = 0, sum = 0;
+#pragma unroll
     for (unsigned k = 0; k < kCluster; ++k) {
-        const int64_t y = *cl.map_shared_rank(&sh.total, k);
+        const int64_t y = sh.totals[k];
         before += k < cl.block_rank() ? y : 0;
         sum += y;
     }
-    cl.sync();  // `total` may be rewritten after this
     all = sum;
     return before + x;
 }
@@ -212,20 +222,18 @@ __device__ __forceinline__ int owner(const int* prefix, int n, int r) {
     return lo;
 }
 
-__global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
-    kv_reserve_kernel(const KvPagesArgs a, int* status) {
-    __shared__ Shared sh;
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) kv_reserve_kernel(const KvPagesArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Reserve& sh = *reinterpret_cast<Reserve*>(smem);
     cg::cluster_group cl = cg::this_cluster();
     pdl_launch_dependents();
     pdl_wait();
     clear_seen(sh, a.max_seqs);
-    for (int i = threadIdx.x; i < MXQ_KV_MAX_SEQS / 32; i += kThreads) sh.cow[i] = 0;
-    __syncthreads();
     int code = 0;
-    // four consecutive sequences a thread, so that one scan gives the prefixes
+    // four consecutive sequences a thread, so that one scan gives the prefixes: of pages (low half) and of
+    // copies (from bit 40), and of tokens
     constexpr int PER = MXQ_KV_MAX_SEQS / kThreads;
-    int need[PER], add[PER];
-    int64_t needs = 0, adds = 0;
+    int64_t need[PER], add[PER], needs = 0, adds = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int i = threadIdx.x * PER + k;
@@ -242,34 +250,33 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
             code = min(code, kBadLength);
             continue;
         }
-        add[k] = static_cast<int>(more);
+        add[k] = more;
         need[k] = pages_for(len + more, a.page_size) - pages_for(len, a.page_size);
         if (more > 0 && len % a.page_size != 0) {
             const int pg = a.table[s * a.table_stride + len / a.page_size];
-            if (pg < 0 || pg >= a.num_pages) {
+            if (pg < 0 || pg >= a.num_pages)
                 code = min(code, kBadIndex);
-            } else if (a.refs[pg] > 1) {  // a shared page that is not full is copied before it is written
-                ++need[k];
-                atomicOr(&sh.cow[i >> 5], 1u << (i & 31));
-            }
+            else if (a.refs[pg] > 1)  // a shared page that is not full is copied before it is written
+                need[k] += 1 + (int64_t(1) << 40);
         }
         needs += need[k];
-        adds += more;
+        adds += add[k];
     }
     int64_t want, tokens;
     int64_t n0 = block_scan(needs, sh, want), a0 = block_scan(adds, sh, tokens);
+    const int copies = static_cast<int>(want >> 40);
+    want &= (int64_t(1) << 40) - 1;
     if (want > a.num_pages) code = min(code, kNoPages);
-    if (a.slots && tokens > a.slots_cap) code = min(code, kBadLength);
-    if (code < 0 || tokens > 0x7fffffff) atomicMin(&sh.verdict, code < 0 ? code : kBadLength);
-    __syncthreads();
-    code = sh.verdict;
+    if ((a.slots && tokens > a.slots_cap) || tokens > 0x7fffffff) code = min(code, kBadLength);
+    code = agree(sh, code);
     if (code == 0) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = threadIdx.x * PER + k;
             if (i > a.n) break;
-            sh.need[i] = static_cast<int>(n0);
+            sh.need[i] = static_cast<int>(n0 & ((int64_t(1) << 40) - 1));
             sh.add[i] = static_cast<int>(a0);
+            if (i < a.n) sh.copy[i] = need[k] >> 40 ? static_cast<uint16_t>(n0 >> 40) : kNoCopy;
             n0 += need[k];
             a0 += add[k];
         }
@@ -283,59 +290,50 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
     const int each = (a.num_pages + kAll - 1) / kAll;
     const int p0 = static_cast<int>(min(static_cast<int64_t>(me) * each, static_cast<int64_t>(a.num_pages)));
     const int p1 = min(p0 + each, a.num_pages);
-    int64_t free_pages = 0;
-    if (code == 0 && want > 0)
+    int64_t rank = 0, have = 0;
+    if (code == 0 && want > 0) {  // (every CTA comes to the same verdict and count)
+        int64_t free_pages = 0;
         for (int p = p0; p < p1; ++p) free_pages += a.refs[p] == 0;
-    int64_t have;
-    int64_t rank = cluster_scan(free_pages, sh, have);  // also: every CTA has read lens, table and refs
-    if (code == 0 && have < want) code = kNoPages;
+        rank = cluster_scan(free_pages, sh, 0, have);  // also: every CTA has read lens, table and refs
+        if (have < want) code = kNoPages;
+    }
     if (me == 0) {
         a.info[0] = code;
         a.info[1] = code < 0 ? 0 : static_cast<int>(want);
-        int copies = 0;
-        if (code == 0)
-            for (int i = 0; i < MXQ_KV_MAX_SEQS / 32; ++i) copies += __popc(sh.cow[i]);
-        a.pairs[0] = copies;
+        a.pairs[0] = code < 0 ? 0 : copies;
     }
-    if (code < 0) {
-        for (int i = me; i < (a.slots ? a.slots_cap : 0); i += kAll) a.slots[i] = -1;
-        return;
-    }
-    if (want > 0)
+    if (code == 0 && want > 0)
         for (int p = p0; p < p1 && rank < want; ++p) {
             if (a.refs[p] != 0) continue;
             const int i = owner(sh.need, a.n, static_cast<int>(rank)), k = static_cast<int>(rank) - sh.need[i];
-            const int s = a.seqs[i], len = a.lens[s];
-            const bool copy = sh.cow[i >> 5] >> (i & 31) & 1u;
-            int* at = a.table + s * a.table_stride + (copy ? len / a.page_size : pages_for(len, a.page_size)) + k;
-            if (copy && k == 0) {
-                const int old = *at;
-                int c = __popc(sh.cow[i >> 5] & ((1u << (i & 31)) - 1u));
-                for (int x = 0; x < (i >> 5); ++x) c += __popc(sh.cow[x]);
-                a.pairs[1 + 2 * c] = old;
-                a.pairs[2 + 2 * c] = p;
+            const int s = a.seqs[i], len = a.lens[s], copy = sh.copy[i];
+            int* at = a.table + s * a.table_stride + (copy != kNoCopy ? len / a.page_size : pages_for(len, a.page_size)) + k;
+            if (copy != kNoCopy && k == 0) {
+                a.pairs[1 + 2 * copy] = *at;
+                a.pairs[2 + 2 * copy] = p;
             }
             *at = p;
             a.refs[p] = 1;  // only this thread looks at p
             ++rank;
         }
     cl.sync();
-    // a copied page loses a holder, only now that no thread looks for free pages any more
-    int copies = 0;
-    for (int i = 0; i < MXQ_KV_MAX_SEQS / 32; ++i) copies += __popc(sh.cow[i]);
-    for (int i = me; i < copies; i += kAll) atomicSub(&a.refs[a.pairs[1 + 2 * i]], 1);
-    if (a.slots) {
-        for (int i = me; i < a.slots_cap; i += kAll) {
-            int slot = -1;
-            if (i < tokens) {
-                const int o = owner(sh.add, a.n, i), s = a.seqs[o], pos = a.lens[s] + i - sh.add[o];
-                slot = a.table[s * a.table_stride + pos / a.page_size] * a.page_size + pos % a.page_size;
-            }
-            a.slots[i] = slot;
-        }
-        cl.sync();
+    if (cl.block_rank() != 0) return;  // what is left is short: one CTA, so that its own barrier orders it
+    if (code < 0) {
+        for (int i = threadIdx.x; i < (a.slots ? a.slots_cap : 0); i += kThreads) a.slots[i] = -1;
+        return;
     }
-    for (int i = me; i < a.n; i += kAll) a.lens[a.seqs[i]] += a.other[i];
+    // a copied page loses a holder, only now that no thread looks for free pages any more
+    for (int i = threadIdx.x; i < copies; i += kThreads) atomicSub(&a.refs[a.pairs[1 + 2 * i]], 1);
+    for (int i = threadIdx.x; i < (a.slots ? a.slots_cap : 0); i += kThreads) {
+        int slot = -1;
+        if (i < tokens) {
+            const int o = owner(sh.add, a.n, i), s = a.seqs[o], pos = a.lens[s] + i - sh.add[o];
+            slot = a.table[s * a.table_stride + pos / a.page_size] * a.page_size + pos % a.page_size;
+        }
+        a.slots[i] = slot;
+    }
+    __syncthreads();  // lengths change once nobody reads them any more
+    for (int i = threadIdx.x; i < a.n; i += kThreads) a.lens[a.seqs[i]] += a.other[i];
 }
 
 // Pages in use behind the first `live` move into the holes among those: the i-th such page into the
@@ -351,7 +349,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) kv_compac
     const int p1 = min(p0 + each, a.num_pages);
     int64_t n = 0, live;
     for (int p = p0; p < p1; ++p) n += a.refs[p] > 0;
-    cluster_scan(n, sh, live);
+    cluster_scan(n, sh, 0, live);
     int64_t movers = 0, holes = 0;
     for (int p = p0; p < p1; ++p) {
         const bool used = a.refs[p] > 0;
@@ -359,7 +357,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) kv_compac
         holes += !used && p < live;
     }
     int64_t moves;
-    int64_t at = cluster_scan(movers << 32 | holes, sh, moves);
+    int64_t at = cluster_scan(movers << 32 | holes, sh, 1, moves);
     int src = static_cast<int>(at >> 32), dst = static_cast<int>(at & 0xffffffff);
     for (int p = p0; p < p1; ++p) {
         const bool used = a.refs[p] > 0;
@@ -425,13 +423,14 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 template <typename K, typename... A>
-int launch(K kernel, int grid, int threads, cudaStream_t st, A... args) {
+int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -445,26 +444,34 @@ int move_grid(int64_t most, int64_t layers, int64_t page_bytes) {
 
 }  // namespace
 
-int launch_kv_fork(const KvPagesArgs& a, cudaStream_t st) { return launch(kv_fork_kernel, kCluster, kThreads, st, a, status_ptr()); }
+int launch_kv_fork(const KvPagesArgs& a, cudaStream_t st) { return launch(kv_fork_kernel, kCluster, kThreads, 0, st, a, status_ptr()); }
 
 int launch_kv_truncate(const KvPagesArgs& a, cudaStream_t st) {
-    return launch(kv_truncate_kernel, kCluster, kThreads, st, a, status_ptr());
+    return launch(kv_truncate_kernel, kCluster, kThreads, 0, st, a, status_ptr());
 }
 
 int launch_kv_reserve(const KvPagesArgs& a, uint8_t* cache, int64_t layers, int64_t layer_stride, int64_t page_bytes,
                       cudaStream_t st) {
-    const int rc = launch(kv_reserve_kernel, kCluster, kThreads, st, a, status_ptr());
+    static std::atomic<int> known[64];  // devices that allow the kernel its shared memory
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ERR_CUDA;
+    if (known[dev].load() == 0) {
+        if (cudaFuncSetAttribute(kv_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Reserve)) != cudaSuccess)
+            return MXQ_ERR_CUDA;
+        known[dev].store(1);
+    }
+    const int rc = launch(kv_reserve_kernel, kCluster, kThreads, sizeof(Reserve), st, a);
     if (rc != MXQ_OK) return rc;
-    return launch(kv_move_kernel<false>, move_grid(a.n, layers, page_bytes), kCopyThreads, st, a, cache, layers, layer_stride,
+    return launch(kv_move_kernel<false>, move_grid(a.n, layers, page_bytes), kCopyThreads, 0, st, a, cache, layers, layer_stride,
                   page_bytes, static_cast<const int*>(nullptr));
 }
 
 int launch_kv_compact(const KvPagesArgs& a, uint8_t* cache, int64_t layers, int64_t layer_stride, int64_t page_bytes,
                       cudaStream_t st) {
     int* map = a.pairs + 1 + 2 * static_cast<int64_t>(a.num_pages);
-    const int rc = launch(kv_compact_kernel, kCluster, kThreads, st, a, map);
+    const int rc = launch(kv_compact_kernel, kCluster, kThreads, 0, st, a, map);
     if (rc != MXQ_OK) return rc;
-    return launch(kv_move_kernel<true>, sm_count() * 8, kCopyThreads, st, a, cache, layers, layer_stride, page_bytes,
+    return launch(kv_move_kernel<true>, sm_count() * 8, kCopyThreads, 0, st, a, cache, layers, layer_stride, page_bytes,
                   static_cast<const int*>(map));
 }
 
