@@ -11,8 +11,8 @@ constexpr int kThreads = 256;
 
 // A warp takes 32 / (D / 32) consecutive tokens of one head and side, a lane 32 elements (chunk c) of one
 // of them.  Consecutive tokens mostly have consecutive slots: then the warp's stores cover whole sectors of
-// the unit (a warp over the heads of one token wrote 2-byte pieces of eight units: 19 us for 8192 tokens of
-// 8 x 128 in MXFP4; this 10 us).
+// the unit (a warp over the heads of one token wrote 2-byte pieces of eight units: append and read of 8192
+// tokens of 8 x 128 in MXFP4 took 31.0 us, this way round 26.2 us).
 struct Place {
     uint32_t token, side, head, c;
     bool any;  // the token exists
@@ -41,6 +41,15 @@ struct Exchange {
     uint8_t at[kThreads / 32][32 / (D / 32)][ROW];
 };
 
+// bf16 values change hands through shared memory too: memory is read and written 16 bytes a lane, side by
+// side, while a lane works on 64 contiguous ones (loading those itself, it touched every 32-byte sector
+// twice: 26.2 us for append and read of 8192 tokens, 25.4 us so).  The warp's 2 KB are 128 pieces of 16 bytes, lane l's own
+// being 4 l .. 4 l + 3; piece p lies at p ^ (p / 8 & 3), so that neither way meets a bank twice.
+struct Pieces {
+    uint4 at[kThreads / 32][128];
+};
+__device__ __forceinline__ int piece_at(int p) { return p ^ (p >> 3 & 3); }
+
 // Appending: quantize with the arithmetic of the streaming quantizer and store codes and scales at the
 // token's place in its unit.  Bound: HBM (2 D values read in bf16, written in 4 bits, per token and head).
 template <int FMT, int RULE, int D>
@@ -48,11 +57,28 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
     using U = KvUnit<FMT, D>;
     __shared__ float tabs[FMT == MXQ_NVFP4 ? 4 : 1][128];
     __shared__ __align__(8) Exchange<D> ex;
+    __shared__ Pieces pieces;
     pdl_launch_dependents();
     pdl_wait();
     const Place p = place_of<D>(a.tokens, a.heads);
-    const uint32_t c = p.c, side = p.side;
+    const uint32_t c = p.c, side = p.side, lane = threadIdx.x & 31;
     int slot = p.any ? a.slots[p.token] : -1;
+    {
+        constexpr int ROW = D / 8;  // pieces of a token
+        uint4* mine = pieces.at[threadIdx.x >> 5];
+        const uint32_t token0 = p.token - lane / (D / 32);
+        const __nv_bfloat16* src = (side ? a.v : a.k) + static_cast<int64_t>(p.head) * a.head_stride[side];
+        uint4 x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t i = q * 32 + lane, token = token0 + i / ROW;
+            x[q] = make_uint4(0, 0, 0, 0);
+            if (token < a.tokens)
+                x[q] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(token) * a.token_stride[side]) + i % ROW);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mine[piece_at(q * 32 + lane)] = x[q];
+    }
     float g[2] = {1.0f, 1.0f};
     if constexpr (FMT == MXQ_NVFP4) {
         g[0] = *a.g_k;
@@ -65,13 +91,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
         kv_status(a.status, kStatusKvSlot);
         slot = -1;
     }
+    __syncwarp();
     uint32_t w[16], codes[4] = {0, 0, 0, 0}, seen = 0, sf = 0;
     if (slot >= 0) {
-        const __nv_bfloat16* src = (side ? a.v : a.k) + static_cast<int64_t>(p.token) * a.token_stride[side] +
-                                   static_cast<int64_t>(p.head) * a.head_stride[side] + c * 32;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + q);
+            const uint4 x = pieces.at[threadIdx.x >> 5][piece_at(4 * lane + q)];
             w[4 * q] = x.x;
             w[4 * q + 1] = x.y;
             w[4 * q + 2] = x.z;
@@ -137,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
     using U = KvUnit<FMT, D>;
     using X = Exchange<D>;
     __shared__ __align__(8) X ex;
+    __shared__ Pieces pieces;
     pdl_launch_dependents();
     pdl_wait();
     const Place p = place_of<D>(a.tokens, a.heads);
@@ -204,10 +230,20 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
             codes[2 + q] = prmt(lo, hi, 0x7531u);
         }
     }
-    if (!p.any) return;
-    uint4* dst = reinterpret_cast<uint4*>((side ? a.v_out : a.k_out) + (static_cast<int64_t>(p.token) * a.heads + p.head) * D + c * 32);
+    uint4* mine = pieces.at[threadIdx.x >> 5];
+    const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dst[q] = dequant8_cvt(codes[q], d[q >> 1]);
+    for (int q = 0; q < 4; ++q) mine[piece_at(4 * lane + q)] = dequant8_cvt(codes[q], d[q >> 1]);
+    __syncwarp();
+    constexpr int ROW = D / 8;  // pieces of a token
+    const uint32_t token0 = p.token - lane / (D / 32);
+    __nv_bfloat16* dst = (side ? a.v_out : a.k_out) + static_cast<int64_t>(p.head) * D;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t i = q * 32 + lane, token = token0 + i / ROW;
+        if (token < a.tokens)
+            reinterpret_cast<uint4*>(dst + static_cast<int64_t>(token) * a.heads * D)[i % ROW] = mine[piece_at(i)];
+    }
 }
 
 template <typename K, typename A>

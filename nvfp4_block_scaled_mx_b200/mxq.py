@@ -385,16 +385,14 @@ def kv_cache_shape(num_pages, kv_heads, head_dim, fmt, page_size, layers=None):
 def _call(name, device, stream, *args):
     """The C call `name` on `device` (that of its tensors, whatever the current one is), on `stream` or the
     device's current stream."""
-    fn = getattr(lib(), name)
-    if device.type != "cuda":
-        if stream is None:
-            stream = _stream()
-        rc = fn(*args, stream)
-    elif device.index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
+        if device.type != "cuda":
+            raise ValueError("mxq works on CUDA tensors only (got %s tensors)" % device)
         with torch.cuda.device(device):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+            rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise MxqError(rc, name)
 
@@ -408,41 +406,38 @@ def _at(t, name, dtype, n, device):
     """Pointer of a contiguous tensor of at least n elements of dtype on the call's device (None passes)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.device == device and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise MxqBufferError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if t.numel() < n:
-        raise MxqBufferError("%s holds %d values, the call needs %d" % (name, t.numel(), n))
     if t.device != device:
         raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
-    return _ptr(t)
+    if t.numel() < n:
+        raise MxqBufferError("%s holds %d values, the call needs %d" % (name, t.numel(), n))
+    raise MxqBufferError("%s must be contiguous" % name)
 
 
 def _rows(t, name, device):
     """[tokens, heads, dim] bf16 whose last dimension is contiguous: pointer, token stride, head stride.  (The
     stride of a dimension of one entry is never used; torch leaves anything there.)"""
-    if t.dtype is not _BF16:
-        raise MxqBufferError("%s must be torch.bfloat16 (got %s)" % (name, t.dtype))
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
+    if t.dtype is not _BF16:
+        raise MxqBufferError("%s must be torch.bfloat16 (got %s)" % (name, t.dtype))
     if s2 != 1 and d > 1:
         raise MxqBufferError("%s needs a contiguous last dimension" % name)
     if t.device != device:
         raise MxqBufferError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
-    return _ptr_strided(t), (s0 if n > 1 else 0), (s1 if h > 1 else 0)
-
-
-def _ptr_strided(t):
-    if not t.is_cuda:
-        raise ValueError("mxq works on CUDA tensors only (got a %s tensor)" % t.device)
-    return t.data_ptr()
+    return t.data_ptr(), (s0 if n > 1 else 0), (s1 if h > 1 else 0)
 
 
 def _kv_layer(cache, head_dim, f):
     """(pages, kv_heads, page_size) of one layer of the cache."""
-    if cache.dtype is not _U8 or cache.dim() != 4:
+    shape = cache.shape
+    if cache.dtype is not _U8 or len(shape) != 4:
         raise MxqBufferError("cache must be uint8 [pages, kv_heads, page_size / 16, unit] (got %s %s)" %
-                             (cache.dtype, tuple(cache.shape)))
-    pages, heads, units, unit = cache.shape
+                             (cache.dtype, tuple(shape)))
+    pages, heads, units, unit = shape
     if unit != _KV_UNIT.get((f, head_dim), unit):  # (what the table does not hold, the library refuses)
         raise MxqBufferError("a unit of the cache holds %d bytes, heads of %d take %d" % (unit, head_dim, _KV_UNIT[f, head_dim]))
     return pages, heads, 16 * units
@@ -461,7 +456,7 @@ def kv_append(k, v, cache, slots, fmt, rule=CEIL, g_k=None, g_v=None, stream=Non
     kp, ks, kh = _rows(k, "k", dev)
     vp, vs, vh = _rows(v, "v", dev)
     _call("mxq_kv_append", dev, stream, kp, vp, T, H, D, ks, kh, vs, vh, _at(slots, "slots", _I32, T, dev), f, _rule(rule),
-          _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _ptr(cache), pages, page_size)
+          _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _at(cache, "cache", _U8, 0, dev), pages, page_size)
 
 
 def kv_read(cache, slots, fmt, head_dim, g_k=None, g_v=None, k_out=None, v_out=None, stream=None):
@@ -469,12 +464,14 @@ def kv_read(cache, slots, fmt, head_dim, g_k=None, g_v=None, k_out=None, v_out=N
     f, dev = _fmt(fmt), cache.device
     pages, H, page_size = _kv_layer(cache, head_dim, f)
     T = slots.numel()
-    if k_out is None:
+    if k_out is None and v_out is None:  # one allocation
+        k_out, v_out = torch.empty((2, T, H, head_dim), dtype=_BF16, device=dev).unbind(0)
+    elif k_out is None:
         k_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
-    if v_out is None:
+    elif v_out is None:
         v_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
     n = T * H * head_dim
-    _call("mxq_kv_read", dev, stream, _ptr(cache), pages, page_size, H, head_dim, f, _at(slots, "slots", _I32, T, dev), T,
+    _call("mxq_kv_read", dev, stream, _at(cache, "cache", _U8, 0, dev), pages, page_size, H, head_dim, f, _at(slots, "slots", _I32, T, dev), T,
           _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _at(k_out, "k_out", _BF16, n, dev),
           _at(v_out, "v_out", _BF16, n, dev))
     return k_out, v_out
@@ -502,7 +499,7 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     qp, qs, qh = _rows(q, "q", dev)
     batch, cols = block_table.shape
     t0, t1 = block_table.stride()
-    if (t1 != 1 and cols > 1) or block_table.dtype is not _I32 or block_table.device != dev or cache.device != dev:
+    if (t1 != 1 and cols > 1) or block_table.dtype is not _I32 or block_table.device != dev:
         raise MxqBufferError("block_table must be torch.int32 [batch, pages] with contiguous rows, on the call's device")
     if out is None:
         out = torch.empty((rows, heads, D), dtype=out_dtype, device=dev)
@@ -514,8 +511,8 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     if workspace is None:
         with _on(q):
             workspace = torch.empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), dtype=_U8, device=dev)
-    _call("mxq_kv_attention", dev, stream, qp, rows, qs, qh, _ptr(cache), pages, page_size, heads, kv_heads, D, f,
-          _ptr_strided(block_table), t0 if batch > 1 else max(cols, 1), cols, _at(kv_lens, "kv_lens", _I32, batch, dev),
+    _call("mxq_kv_attention", dev, stream, qp, rows, qs, qh, _at(cache, "cache", _U8, 0, dev), pages, page_size, heads, kv_heads, D, f,
+          block_table.data_ptr(), t0 if batch > 1 else max(cols, 1), cols, _at(kv_lens, "kv_lens", _I32, batch, dev),
           batch, _at(q_start, "q_start", _I32, batch + 1, dev), max_q, D ** -0.5 if scale is None else scale, causal, window,
           _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), dtype is _F32,
           _at(out, "out", dtype, rows * heads * D, dev), _at(lse, "lse", _F32, rows * heads, dev),

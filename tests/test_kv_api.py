@@ -121,20 +121,8 @@ def test_page_refusals(L, call):
 
 def test_binding_guards(monkeypatch):
     mxq_build.build()
-    real, calls = mxq.lib(), []
-
-    class Rec:
-        def __getattr__(self, name):
-            if name in ("mxq_kv_append", "mxq_kv_read", "mxq_kv_attention", "mxq_kv_reserve", "mxq_kv_fork", "mxq_kv_truncate",
-                        "mxq_kv_compact"):
-                return lambda *a: calls.append(name) or 0
-            return getattr(real, name)
-
-    rec = Rec()
-    monkeypatch.setattr(mxq, "lib", lambda: rec)
-    for name in ("_ptr", "_ptr_strided"):
-        monkeypatch.setattr(mxq, name, lambda t: None if t is None else 0)
-    monkeypatch.setattr(mxq, "_stream", lambda stream=None: None)
+    calls = []
+    monkeypatch.setattr(mxq, "_call", lambda name, device, stream, *args: calls.append(name))
     i32 = lambda *x: torch.zeros(x, dtype=torch.int32)  # noqa: E731
     bf = lambda *x: torch.zeros(x, dtype=torch.bfloat16)  # noqa: E731
     cache = torch.zeros(mxq.kv_cache_shape(4, 2, 64, "mxfp4", 32), dtype=torch.uint8)
@@ -176,7 +164,18 @@ def test_binding_guards(monkeypatch):
                 lambda: mxq.kv_fork(i32(2), i32(2), state[0], i32(2), state[2], 32),
                 lambda: mxq.kv_truncate(i32(2), i32(2).long(), *state, 32),
                 lambda: mxq.kv_truncate(i32(2), i32(2), *state, 32, info=i32(1)),
+                lambda: mxq.kv_append(k, k, cache[:, :, :, ::2], i32(5), "mxfp4"),
+                lambda: mxq.kv_append(k, k, cache.transpose(0, 2), i32(5), "mxfp4"),
                 lambda: mxq.kv_compact(*state, cache[:3], 32)):
         with pytest.raises(ValueError):
             bad()
     assert len(calls) == n
+
+
+def test_host_tensors_are_refused():
+    if torch.cuda.is_available():
+        pytest.skip("a device is there: the call would name it")
+    cache = torch.zeros(mxq.kv_cache_shape(4, 2, 64, "mxfp4", 32), dtype=torch.uint8)
+    k = torch.zeros((5, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises((ValueError, AssertionError, RuntimeError)):
+        mxq.kv_append(k, k, cache, torch.zeros(5, dtype=torch.int32), "mxfp4")
