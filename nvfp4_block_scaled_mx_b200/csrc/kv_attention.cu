@@ -30,17 +30,8 @@ namespace {
 
 constexpr int kWarps = 4;                     // warps that compute; one more feeds them
 constexpr int kThreads = (kWarps + 1) * 32;
-#ifndef C_NTMAX
-#define C_NTMAX 3
-#endif
-#ifndef C_MINT
-#define C_MINT 4
-#endif
-constexpr int kMinTiles = C_MINT;  // token tiles a CTA gets at least
-#ifndef C_EX
-#define C_EX 10
-#endif
-constexpr int kExtraTiles = C_EX;  // counted for beginning a row tile
+constexpr int kMinTiles = 4;     // token tiles a CTA gets at least (4 of 4, 8 and 12: 11.6, 12.0, 12.4 us for one sequence of 1009)
+constexpr int kExtraTiles = 10;  // counted for beginning a row tile (32 sequences of 500 to 16000: 56.6 us at 0, 51.3 at 6, 49.4 at 10)
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -754,11 +745,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 
 // --------------------------------------------------------------------------------------- host
 
-// n-tiles of eight rows: as few as hold a sequence's rows, at most what the registers hold.
-int n_tiles(int64_t rows, int D) {
-    if (rows <= 8) return 1;
-    if (rows <= 16 || D == 256) return 2;
-    return C_NTMAX;
+// n-tiles of eight rows a CTA takes at once, one or two: the second one costs 8/9 of the first (its K and V are
+// decoded already), but the last row tile pads to 16 rows (head size 256, 20 rows: 100 us with one, 118 with
+// two; 10 rows: 71 and 66; 500 rows: 1814 and 1618).  Three or four leave room for half the warps (MXFP4, a chunk
+// of 700 tokens: 772 us with two, 855 and 817 with three and four).
+int n_tiles(int64_t rows) { return 9 * ((rows + 7) / 8) < 16 * ((rows + 15) / 16) ? 1 : 2; }
+
+// Rows from which a row tile on tcgen05 (32 rows for NVFP4 with head size 128, else 128) takes less time.  16
+// sequences of 3000 to 4100, 8 kv heads, here and there, in us: NVFP4, 128 wide, 10 rows 35 and 47, 20 rows 54 and
+// 48, 65 rows 115 and 77; 64 wide, 35 rows 50 and 61, 65 rows 73 and 62; MXFP4, 128 wide, 35 rows 79 and 103, 65 rows
+// 122 and 106, 500 rows 688 and 339; 64 wide, 65 rows 76 and 82, 500 rows 402 and 262.
+bool on_tcgen05(int fmt, int D, int64_t rows) {
+    return D <= 128 && rows > (fmt == MXQ_NVFP4 && D == 128 ? 16 : 64);
 }
 
 constexpr int kMaxCtasPerSm = 4;
@@ -801,8 +799,8 @@ int run(KvAttnArgs& a, cudaStream_t st) {
 
 template <int FMT>
 int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
-    if (D == 64) return nt == 1 ? run<FMT, 64, 1>(a, st) : nt == 2 ? run<FMT, 64, 2>(a, st) : run<FMT, 64, C_NTMAX>(a, st);
-    if (D == 128) return nt == 1 ? run<FMT, 128, 1>(a, st) : nt == 2 ? run<FMT, 128, 2>(a, st) : run<FMT, 128, C_NTMAX>(a, st);
+    if (D == 64) return nt == 1 ? run<FMT, 64, 1>(a, st) : run<FMT, 64, 2>(a, st);
+    if (D == 128) return nt == 1 ? run<FMT, 128, 1>(a, st) : run<FMT, 128, 2>(a, st);
     return nt == 1 ? run<FMT, 256, 1>(a, st) : run<FMT, 256, 2>(a, st);
 }
 
@@ -811,15 +809,15 @@ int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
 size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_heads, int D) {
     (void)batch;
     const int64_t rows = max_q * (heads / kv_heads);
-    const size_t here = static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * 8 * n_tiles(rows, D) * (D + 2) * 4 + sizeof(Split));
+    const size_t here = static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * 8 * n_tiles(rows) * (D + 2) * 4 + sizeof(Split));
     const size_t there = static_cast<size_t>(sm_count()) * (2 * kv_rows_tile(rows) * (D + 2) * 4 + sizeof(Split));
-    return rows > 8 && D <= 128 ? std::max(here, there) : here;
+    return rows > 16 && D <= 128 ? std::max(here, there) : here;
 }
 
 int launch_kv_attention(int fmt, int D, KvAttnArgs& a, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.max_q) * a.group;
-    if (rows > 8 && fmt == MXQ_NVFP4 && D <= 128) return launch_kv_attention_rows(D, a, st);
-    const int nt = n_tiles(rows, D);
+    if (on_tcgen05(fmt, D, rows)) return launch_kv_attention_rows(fmt, D, a, st);
+    const int nt = n_tiles(rows);
     return fmt == MXQ_NVFP4 ? run_dim<MXQ_NVFP4>(D, nt, a, st) : run_dim<MXQ_MXFP4>(D, nt, a, st);
 }
 

@@ -1,22 +1,31 @@
-// kv_attention_rows.cu -- attention over the paged 4-bit cache for sequences with more than eight rows
-// (query token x query head of a kv head's group): drafted tokens, chunks of a prefill.
+// kv_attention_rows.cu -- attention over the paged 4-bit cache for sequences with many rows (query token x
+// query head of a kv head's group): drafted tokens, chunks of a prefill.  on_tcgen05 in kv_attention.cu says
+// from how many rows on.
 //
 // With many rows the tensor work counts, so it runs on tcgen05 (kind::f16, fp32 accumulators in TMEM), one
 // CTA per SM, tiles of 128 tokens:
-//   S = Q K^T   Q [128 rows x D] in TMEM (the A operand, written once per segment), K decoded into shared
-//               memory as f16 (codes times E4M3 scale, exact), 128-byte swizzle;
+//   S = Q K^T   Q [128 rows x D] and K in shared memory, 128-byte swizzle; Q once per segment, f16 times a power
+//               of two per row; K as f16, codes times scale: E4M3 (exact), E8M0 relative to the token's largest
+//               (exact down to 2^-27 of it), which the softmax multiplies S by;
 //   P = 2^(s - base), f16, in TMEM; one thread has one row, so the softmax needs no shuffles;
-//   O += P V    V decoded as f16 into shared memory transposed ([channel][token]).
+//   O += P V    V decoded as f16 into shared memory transposed ([channel][token]); E8M0 scales relative to a
+//               running reference per 32 channels (blocks 2^23 below it vanish), which O follows.
 // Roles: two groups of 4 softmax warps (their TMEM lanes are the rows) that take the tiles in turn, each with
 // its own S and O, so that one group's exponentials run beside the other's products; 4 warps that decode K
 // (32 tokens of a tile each) and 8 that decode V (16 tokens); one warp that feeds raw tiles by bulk copies;
 // one that issues the MMAs.  P takes the place of S's first half: chunk by chunk of 32 tokens the scores are
 // read, and their probabilities written where scores have been read already.
-// QUAD (up to 32 rows): the rows stand four times in the lanes, and each softmax warp takes 32 of the tile's
+// QUAD (NVFP4, up to 32 rows): the rows stand four times in the lanes, and each softmax warp takes 32 of the tile's
 // 128 tokens, the others' P columns being zero: the four partial results join at the end, like CTAs' parts.
 // The base of a row follows its maximum only when a probability would pass 2^15 (f16 ends at 2^16); O and
 // the tile's earlier P are rescaled in TMEM then.  Work is cut over the CTAs as in kv_attention.cu, with the
 // same join kernel.
+//
+// What bounds it: the softmax groups.  A tile takes a group about 4400 cycles (128 scores a thread: four reads
+// of TMEM, 128 exponentials at 8 cycles a warp, conversions, maxima), of which the tensor work is 1000 and the
+// decoding, on other warps, 2300.  A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of
+// 128): 220 us for NVFP4 (515 TFLOP/s), 317 for MXFP4, whose value warps also agree on references tile by tile.
+// Four drafted tokens for each of 16 sequences of 3000 to 4100: 48 us.
 #include <algorithm>
 #include <atomic>
 
@@ -31,10 +40,7 @@ constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
 constexpr int kRowThreads = (kMmaWarp + 1) * 32;
 constexpr int kTokens = 128;  // of a tile
 constexpr int kMinRowTiles = 2;
-#ifndef C_EXR
-#define C_EXR 8
-#endif
-constexpr int kExtraRowTiles = C_EXR;  // counted for beginning a row tile
+constexpr int kExtraRowTiles = 8;  // counted for beginning a row tile (a chunk of 700: 229 us at 0, 226 at 4, 219 at 8)
 constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^7; above 2^15 it is raised
 
 template <int FMT, int D, bool QUAD>
@@ -48,26 +54,31 @@ struct RCfg {
     static constexpr int OFF_K = 0;  // 1024-byte aligned, as the others
     static constexpr int OFF_V = OFF_K + 2 * K16;
     static constexpr int OFF_Q = OFF_V + 2 * V16;  // QUAD: at a segment's end also [4][32][MERGE] floats
-    static constexpr int MERGE = D == 128 ? 33 : 17;  // a column slice and a skew
-    static_assert(4 * 32 * MERGE * 4 <= Q16, "merge buffer");
+    static constexpr int MERGE = 33;               // floats: a slice of 32 channels and a skew
+    static_assert(!QUAD || (FMT == MXQ_NVFP4 && D == 128 && 4 * 32 * MERGE * 4 <= Q16), "what is joined in one CTA");
     static constexpr int OFF_RAW = OFF_Q + Q16;
     static constexpr int OFF_ML = OFF_RAW + STAGES * RAW;  // [2 groups][128 lanes] (base, l)
     static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // scale of each row's scores
-    static constexpr int OFF_SEG = OFF_QS + 128 * 4;
+    // MXFP4: of the last four tiles, each token's key factor, and the reference codes and largest codes of V's blocks
+    static constexpr int OFF_KF = OFF_QS + 128 * 4;
+    static constexpr int OFF_REF = OFF_KF + (FMT == MXQ_MXFP4 ? 4 * kTokens * 4 : 0);
+    static constexpr int OFF_MAX = OFF_REF + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
+    static constexpr int OFF_SEG = OFF_MAX + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
     static constexpr int OFF_BAR = OFF_SEG + 2 * 64;
-    static constexpr int NBARS = 2 * STAGES + 10 + 1 + 4;
+    static constexpr int NBARS = 2 * STAGES + 12 + 1 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int BYTES = OFF_TMEM + 16 + 1024;  // and the alignment
     static constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each: S 128 columns, O D columns
 };
 
 struct RowBars {
-    uint64_t *raw_full, *raw_empty, *kf, *vf, *sf, *pf, *od, *qf, *seg_full, *seg_empty;
+    uint64_t *raw_full, *raw_empty, *kf, *vf, *sf, *pf, *od, *vm, *qf, *seg_full, *seg_empty;
     __device__ __forceinline__ RowBars(uint8_t* at, int stages) {
         uint64_t* b = reinterpret_cast<uint64_t*>(at);
         raw_full = b, raw_empty = b + stages, b += 2 * stages;
         // of tile n, at n & 1: K and V decoded, S done (K may be overwritten), P written, O done (V, P may be)
-        kf = b, vf = b + 2, sf = b + 4, pf = b + 6, od = b + 8, b += 10;
+        // (MXFP4: vm, the largest codes of V's blocks are there)
+        kf = b, vf = b + 2, sf = b + 4, pf = b + 6, od = b + 8, vm = b + 10, b += 12;
         qf = b, b += 1;
         seg_full = b, seg_empty = b + 2;
     }
@@ -229,6 +240,7 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
                                  smem_desc(k + at, 16, 1024, kLayoutSwizzle128B), IDESC_S, j == 0 ? 0u : 1u);
                     }
                     tc_commit(&bar.sf[t & 1]);
+                    if constexpr (FMT == MXQ_MXFP4) mbar_arrive(&bar.sf[t & 1]);  // hands the keys' factors on
                 }
                 __syncwarp();
             }
@@ -239,10 +251,23 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
     }
 }
 
+// MXFP4 scale codes of a token's key blocks, one a byte (0 behind the last), and the largest of them.
+template <int D>
+__device__ __forceinline__ uint32_t key_codes(uint32_t at) {
+    if constexpr (D == 64) return ld_shared_u16(at);
+    uint32_t x[1];
+    lds<4>(at, x);
+    return x[0];
+}
+__device__ __forceinline__ uint32_t largest_code(uint32_t c) {
+    const uint32_t m = __vmaxu2(c & 0x00FF00FFu, c >> 8 & 0x00FF00FFu);
+    return max(m & 0xFFFFu, m >> 16);
+}
+
 // Keys of units u, u + 1: a lane has quarter q of token r: 32-bit words of 8 elements, 16 bytes each once
 // decoded.  Eight neighbouring lanes have four tokens and two quarters, whose chunks meet different banks.
 template <int FMT, int D, bool QUAD>
-__device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u) {
+__device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u, float* factors) {
     using U = typename RCfg<FMT, D, QUAD>::U;
     const int lane = threadIdx.x & 31;
     const int r0 = (lane >> 3 & 1) * 4 + (lane >> 1 & 3), q = (lane >> 4) * 2 + (lane & 1);
@@ -251,18 +276,36 @@ __device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u) {
     for (int i = 0; i < 4; ++i) {
         const uint32_t unit = raw + (u + i / 2) * U::BYTES;
         const int r = r0 + 8 * (i & 1);
-        sc[i] = D == 128 ? ld_shared_u16(unit + U::OFF_KS + r * U::NB + 2 * q) : ld_shared_u8(unit + U::OFF_KS + r * U::NB + q);
+        if constexpr (FMT == MXQ_NVFP4) {
+            sc[i] = D == 128 ? ld_shared_u16(unit + U::OFF_KS + r * U::NB + 2 * q) : ld_shared_u8(unit + U::OFF_KS + r * U::NB + q);
+        } else {
+            sc[i] = key_codes<D>(unit + U::OFF_KS + r * U::NB);
+        }
         lds<U::W>(unit + U::k_at(r, q, 0), w[i]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t row = u * 16 + 8 * i + r0, f = e4m3x2_f16x2(sc[i]);
+        const uint32_t row = u * 16 + 8 * i + r0;
+        uint32_t f = 0, most = 0;
+        if constexpr (FMT == MXQ_NVFP4)
+            f = e4m3x2_f16x2(sc[i]);
+        else
+            most = largest_code(sc[i]);
+        // S of the token is in units of 2^(most - 127 - 13)
+        if (FMT == MXQ_MXFP4 && q == 0) factors[row] = __uint_as_float(most > 13 ? (most - 13) << 23 : 0u);
 #pragma unroll
         for (int k = 0; k < U::W / 4; ++k) {
-            const uint32_t f2 = k < 2 ? prmt(f, f, 0x1010u) : prmt(f, f, 0x3232u);
+            uint32_t f2, chunk;  // factor of the word's 8 elements, twice; their place in the row
+            if constexpr (FMT == MXQ_NVFP4) {
+                f2 = k < 2 ? prmt(f, f, 0x1010u) : prmt(f, f, 0x3232u);
+                chunk = q * (U::W / 4) + k;
+            } else {  // word k lies in block k: 2^(code - most + 13), exact down to 2^-27 below the token's largest
+                const int field = static_cast<int>(sc[i] >> (8 * k) & 0xFFu) - static_cast<int>(most) + 28;
+                f2 = static_cast<uint32_t>(max(field, 0)) * 0x04000400u;
+                chunk = 4 * k + q;
+            }
             uint32_t o[4];
             e2m1x8(w[i][k], o);
-            const uint32_t chunk = q * (U::W / 4) + k;  // of 8 elements in the row
             st_shared_v4(k16 + (chunk >> 3) * (kTokens * 128) + row * 128 + (((chunk & 7) ^ (r0 & 7)) << 4),
                          make_uint4(hmul2(o[0], f2), hmul2(o[1], f2), hmul2(o[2], f2), hmul2(o[3], f2)));
         }
@@ -271,8 +314,10 @@ __device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u) {
 
 // Values of unit u, transposed: a lane has tokens 8 h + 2 t, + 1 and channels 16 j + 2 g, + 1.
 template <int FMT, int D, bool QUAD>
-__device__ __forceinline__ void values(uint32_t raw, uint32_t v16, int u, bool edge, int pos0, int seen0, int seen1) {
-    using U = typename RCfg<FMT, D, QUAD>::U;
+__device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool edge, int pos0, int seen0, int seen1,
+                                       uint8_t* smem, const RowBars& bar, uint32_t n, int (&ref)[4], int* status) {
+    using C = RCfg<FMT, D, QUAD>;
+    using U = typename C::U;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t unit = raw + u * U::BYTES;
     // channel 16 j + 2 g has swizzle row 2 g, the next one 2 g + 1, whatever j is
@@ -291,7 +336,44 @@ __device__ __forceinline__ void values(uint32_t raw, uint32_t v16, int u, bool e
         for (int h = 0; h < 2; ++h) {
             const uint32_t live = pair_mask(pos0 + 16 * u + 8 * h + 2 * t, seen0, seen1);
 #pragma unroll
-            for (int i = 0; i < PB / 4; ++i) sb[h][i] = __vminu4(sb[h][i] & live & 0x7F7F7F7Fu, 0x7E7E7E7Eu);
+            for (int i = 0; i < PB / 4; ++i) {
+                sb[h][i] &= live;
+                if constexpr (FMT == MXQ_NVFP4) sb[h][i] = __vminu4(sb[h][i] & 0x7F7F7F7Fu, 0x7E7E7E7Eu);
+            }
+        }
+    }
+    uint32_t fac[2][U::NB];  // f16x2 of the two tokens
+    if constexpr (FMT == MXQ_NVFP4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < U::NB; ++b) fac[h][b] = e4m3x2_f16x2(b & 1 ? sb[h][b >> 1] >> 16 : sb[h][b >> 1] & 0xFFFFu);
+    } else {
+        // Factors 2^(code - ref + 9) with a reference per 32 channels that the whole tile shares: the largest
+        // code of the segment so far, moved up when one exceeds it by more than 2 (the softmax warps scale O
+        // then).  The eight warps agree on a tile's largest codes in shared memory.
+        int* most = reinterpret_cast<int*>(smem + C::OFF_MAX) + (n & 3) * 4;
+#pragma unroll
+        for (int b = 0; b < U::NB; ++b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fac[h][b] = prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);  // the codes, one a half
+            const uint32_t m = __vmaxu2(fac[0][b], fac[1][b]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+            if (lane == b) atomicMax(&most[b], static_cast<int>(top));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.vm[n & 1]);
+        if (!wait_warp(&bar.vm[n & 1], n >> 1 & 1u, status, 0x62)) return false;
+        // tile n + 2's, which nobody looks at before all have passed the next wait
+        if (u == 0 && lane < 4) reinterpret_cast<int*>(smem + C::OFF_MAX)[((n + 2) & 3) * 4 + lane] = 0;
+#pragma unroll
+        for (int b = 0; b < U::NB; ++b) {
+            const int top = most[b];
+            if (top > ref[b] + 2) ref[b] = top;
+            const uint32_t bias = static_cast<uint32_t>((24 - ref[b]) & 0xFFFF) * 0x10001u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fac[h][b] = __viaddmax_s16x2_relu(fac[h][b], bias, 0u) << 10;
+            if (u == 0 && lane == b) reinterpret_cast<int*>(smem + C::OFF_REF)[(n & 3) * 4 + b] = ref[b];
         }
     }
 #pragma unroll
@@ -310,12 +392,13 @@ __device__ __forceinline__ void values(uint32_t raw, uint32_t v16, int u, bool e
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int j = 4 * wd + k;
-                const uint32_t f = e4m3x2_f16x2(j & 1 ? sb[h][j >> 1] >> 16 : sb[h][j >> 1] & 0xFFFFu);
+                const uint32_t f = fac[h][FMT == MXQ_NVFP4 ? j : j / 2];
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(hmul2(v0[k], f)) : "memory");
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(hmul2(v1[k], f)) : "memory");
             }
         }
     }
+    return true;
 }
 
 // Decodes tiles to f16 operands: warps 0-3 the keys of two units each, warps 4-11 the values of one.
@@ -335,6 +418,7 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.seg_empty[buf]);
         if (count < 0) return;
+        int ref[4] = {-1000, -1000, -1000, -1000};  // MXFP4: E8M0 codes that stand for 2^9 in V's factors
 #pragma unroll 1
         for (int i = 0; i < count; ++i, pos0 += kTokens) {
             const uint32_t n = base + i, slot = n % C::STAGES;
@@ -342,11 +426,13 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
             const uint32_t raw = smem_u32(smem + C::OFF_RAW + slot * C::RAW);
             if (warp < kKeyWarps) {
                 if (!wait_warp(&bar.sf[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5b)) return;
-                keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp);
+                keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp,
+                                   reinterpret_cast<float*>(smem + C::OFF_KF) + (n & 3) * kTokens);
             } else {
                 if (!wait_warp(&bar.od[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5c)) return;
-                values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
-                                     pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1);
+                if (!values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
+                                          pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status))
+                    return;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -356,6 +442,12 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
             }
         }
     }
+}
+
+// A value of O: for MXFP4 relative to its 32 channels' reference code, which stands for 2^9.
+template <int FMT>
+__device__ __forceinline__ float value(uint32_t x, int ref) {
+    return FMT == MXQ_MXFP4 ? scale_pow2(__uint_as_float(x), max(ref, 0) - 136) : __uint_as_float(x);
 }
 
 // Softmax: a thread has one row (QUAD: one row and a quarter of each tile's tokens) in every second tile.
@@ -371,7 +463,8 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     float* partials = a.partial + gridDim.x * (sizeof(Split) / 4);
-    const float qscale = a.scale * 1.4426950408889634f * *a.g_k, gv = *a.g_v;
+    float qscale = a.scale * 1.4426950408889634f, gv = 1.0f;
+    if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k, gv = *a.g_v;
     uint32_t v[32];
 #pragma unroll 1
     for (uint32_t nseg = 0;; ++nseg) {
@@ -448,6 +541,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
         float base = kNegMax, l = 0.0f;
         const uint32_t o_at = lanes + C::O_COL + group * D;
         bool begun = false;  // O holds something
+        int oref[4] = {0, 0, 0, 0};  // MXFP4: the reference codes that O is relative to
         // tiles n with n & 1 = group
 #pragma unroll 1
         for (uint32_t n = note.base + ((note.base ^ group) & 1u); n < note.base + note.count; n += 2) {
@@ -456,6 +550,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 break;
             }
             tc_fence_after();
+            const float* kfac = reinterpret_cast<const float*>(smem + C::OFF_KF) + (n & 3) * kTokens;
             const uint32_t s_at = lanes + C::S_COL + group * 128;
             const int pos0 = note.pos0 + static_cast<int>(n - note.base) * kTokens;
             const bool edge = pos0 < note.all0 || pos0 + kTokens > note.all1;
@@ -465,6 +560,16 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     tmem_ld_32x32b_x32(s_at + 32 * c, v);
                     tmem_ld_wait();
                     float m0 = kNegMax, m1 = kNegMax;
+                    if constexpr (FMT == MXQ_MXFP4) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(kfac + 32 * c + k);
+                            v[k] = __float_as_uint(__uint_as_float(v[k]) * f.x);
+                            v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) * f.y);
+                            v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) * f.z);
+                            v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) * f.w);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), cs, -from));
                     if (edge) {
@@ -532,6 +637,27 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 for (int c = 0; c < 4; ++c)
                     if (c != quad) tmem_st_x16(s_at + 16 * c, z);
             }
+            if constexpr (FMT == MXQ_MXFP4) {  // V's references of this tile; O follows where they moved
+                if (!wait_warp(&bar.vf[group], n >> 1 & 1u, a.status, 0x63)) {
+                    dead = true;
+                    break;
+                }
+                const int* refs = reinterpret_cast<const int*>(smem + C::OFF_REF) + (n & 3) * 4;
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    const int to = refs[b];
+                    if (begun && to != oref[b]) {  // the same for all threads
+                        const float f = scale_pow2(1.0f, max(oref[b] - to, -252));
+                        tmem_ld_32x32b_x32(o_at + 32 * b, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        tmem_st_x16(o_at + 32 * b, v);
+                        tmem_st_x16(o_at + 32 * b + 16, v + 16);
+                    }
+                    oref[b] = to;
+                }
+            }
             begun = true;
             tmem_st_wait();
             tc_fence_before();
@@ -560,7 +686,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
         if constexpr (QUAD) {
             // Threads 8 jr .. 8 jr + 7 join row jr: of the eight results (two groups, four lanes), a slice of
             // the channels each; group 0 reads even slices from TMEM, group 1 odd ones, in turn.
-            constexpr int SL = D / 4;  // channels of a slice (32 or 16)
+            constexpr int SL = 32;  // channels of a slice
             const int jr = threadIdx.x >> 3, jc = (threadIdx.x & 7) * (SL / 8);
             const int jrow = note.row0 + (jr < note.rows ? jr : 0), jj = jrow / a.group;
             const int64_t o = static_cast<int64_t>(note.q0 + jj) * a.heads + note.head * a.group + jrow - jj * a.group;
@@ -571,7 +697,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
             for (int k = 0; k < 8; ++k) sum += ml[k * 32 + jr].y * ex2(ml[k * 32 + jr].x - most);
             float f[4];
 #pragma unroll 1
-            for (int pass = 0; pass < 4; ++pass) {
+            for (int pass = 0; pass < D / SL; ++pass) {
                 float y[SL / 8];
 #pragma unroll
                 for (int k = 0; k < SL / 8; ++k) y[k] = 0.0f;
@@ -579,11 +705,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 for (int gg = 0; gg < 2; ++gg) {
                     if (gg == 0 ? !has0 : !has1) continue;
                     if (group == (pass & 1)) {
-                        if constexpr (SL == 32) {
-                            tmem_ld_32x32b_x32(lanes + C::O_COL + gg * D + pass * SL, v);
-                        } else {
-                            tmem_ld_32x32b_x16(lanes + C::O_COL + gg * D + pass * SL, *reinterpret_cast<uint32_t(*)[16]>(v));
-                        }
+                        tmem_ld_32x32b_x32(lanes + C::O_COL + gg * D + pass * SL, v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < SL; ++k) merge[tl * C::MERGE + k] = __uint_as_float(v[k]);
@@ -601,10 +723,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 const float inv = gv * (sum > 0.0f ? 1.0f / sum : sum);
                 if (note.whole) {
                     if (jr < note.rows) {
-                        if constexpr (SL == 32)
-                            put4(a, o * D + d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-                        else
-                            put2(a, o * D + d, y[0] * inv, y[1] * inv);
+                        put4(a, o * D + d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
                         if (a.lse && d == 0)
                             a.lse[o] = sum == 0.0f ? __int_as_float(0xff800000) : (most + log2f(sum)) * 0.6931471805599453f;
                     }
@@ -616,6 +735,10 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
             }
         } else {
             // each group takes half of the channels
+            // (MXFP4: references of each group's last tile, written before its V was done and kept for four tiles)
+            const int* ref = reinterpret_cast<const int*>(smem + C::OFF_REF);
+            const int *ref0 = ref + ((last & 1) == 0 ? last & 3 : (last - 1) & 3) * 4,
+                      *ref1 = ref + ((last & 1) == 1 ? last & 3 : (last - 1) & 3) * 4;
             const float2 z0 = ml[tl], z1 = ml[128 + tl];
             const float most = fmaxf(z0.x, z1.x), f0 = has0 ? ex2(z0.x - most) : 0.0f, f1 = has1 ? ex2(z1.x - most) : 0.0f;
             const float sum = z0.y * f0 + z1.y * f1;
@@ -630,13 +753,13 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     tmem_ld_32x32b_x16(lanes + C::O_COL + d, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(x[k]) * f0;
+                    for (int k = 0; k < 16; ++k) y[k] = value<FMT>(x[k], FMT == MXQ_MXFP4 ? ref0[d / 32] : 0) * f0;
                 }
                 if (has1) {
                     tmem_ld_32x32b_x16(lanes + C::O_COL + D + d, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = fmaf(__uint_as_float(x[k]), f1, y[k]);
+                    for (int k = 0; k < 16; ++k) y[k] = fmaf(value<FMT>(x[k], FMT == MXQ_MXFP4 ? ref1[d / 32] : 0), f1, y[k]);
                 }
                 if (note.whole) {
                     if (real) {
@@ -677,15 +800,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) kv_attention_rows_kernel(const
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.kf[i], kKeyWarps);
             mbar_init(&bar.vf[i], kValueWarps);
-            mbar_init(&bar.sf[i], 1);
+            mbar_init(&bar.sf[i], FMT == MXQ_MXFP4 ? 2 : 1);
             mbar_init(&bar.pf[i], kSoftWarps / 2);
             mbar_init(&bar.od[i], 1);
+            mbar_init(&bar.vm[i], kValueWarps);
             mbar_init(&bar.seg_full[i], 1);
             mbar_init(&bar.seg_empty[i], kSoftWarps + kDecWarps + 1);
         }
         mbar_init(bar.qf, kSoftWarps);
         fence_barrier_init();
     }
+    if (FMT == MXQ_MXFP4 && threadIdx.x < 16) reinterpret_cast<int*>(smem + C::OFF_MAX)[threadIdx.x] = 0;
     if (warp == kMmaWarp) {
         tmem_alloc(slot, 512);
         tmem_relinquish();
@@ -749,9 +874,10 @@ int run_rows(KvAttnArgs& a, cudaStream_t st) {
 
 int kv_rows_tile(int64_t rows) { return rows <= 32 ? 32 : 128; }
 
-int launch_kv_attention_rows(int D, KvAttnArgs& a, cudaStream_t st) {
+int launch_kv_attention_rows(int fmt, int D, KvAttnArgs& a, cudaStream_t st) {
     const bool quad = kv_rows_tile(static_cast<int64_t>(a.max_q) * a.group) == 32;
-    if (D == 64) return quad ? run_rows<MXQ_NVFP4, 64, true>(a, st) : run_rows<MXQ_NVFP4, 64, false>(a, st);
+    if (fmt == MXQ_MXFP4) return D == 64 ? run_rows<MXQ_MXFP4, 64, false>(a, st) : run_rows<MXQ_MXFP4, 128, false>(a, st);
+    if (D == 64) return run_rows<MXQ_NVFP4, 64, false>(a, st);
     return quad ? run_rows<MXQ_NVFP4, 128, true>(a, st) : run_rows<MXQ_NVFP4, 128, false>(a, st);
 }
 

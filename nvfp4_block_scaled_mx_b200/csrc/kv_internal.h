@@ -53,8 +53,8 @@ struct KvAttnArgs {
 int launch_kv_append(int fmt, int rule, int D, const KvAppendArgs& a, cudaStream_t st);
 int launch_kv_read(int fmt, int D, const KvReadArgs& a, cudaStream_t st);
 int launch_kv_attention(int fmt, int D, KvAttnArgs& a, cudaStream_t st);
-// Sequences of more than eight rows on tcgen05 (NVFP4, head size 64 or 128), and the rows of its row tiles.
-int launch_kv_attention_rows(int D, KvAttnArgs& a, cudaStream_t st);
+// Sequences of more than eight rows on tcgen05 (head size 64 or 128), and the rows of its row tiles.
+int launch_kv_attention_rows(int fmt, int D, KvAttnArgs& a, cudaStream_t st);
 int kv_rows_tile(int64_t rows);
 size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_heads, int D);
 
