@@ -401,7 +401,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
-    int b = plan.b, qt = 0;
+    int b = plan.b, qt = plan.qt;
     Seq s = plan.s;
     float qscale = a.scale * 1.4426950408889634f;
     if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k;

@@ -21,11 +21,14 @@
 // the tile's earlier P are rescaled in TMEM then.  Work is cut over the CTAs as in kv_attention.cu, with the
 // same join kernel.
 //
-// What bounds it: the softmax groups.  A tile takes a group about 4400 cycles (128 scores a thread: four reads
-// of TMEM, 128 exponentials at 8 cycles a warp, conversions, maxima), of which the tensor work is 1000 and the
-// decoding, on other warps, 2300.  A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of
-// 128): 220 us for NVFP4 (515 TFLOP/s), 317 for MXFP4, whose value warps also agree on references tile by tile.
-// Four drafted tokens for each of 16 sequences of 3000 to 4100: 48 us.
+// What bounds it: a tile takes 2200 to 2500 cycles.  The products alone take 1750: eight instructions of S and of
+// P V are issued in 870 cycles each, not the 512 of an idle SM, as K, V and Q are read from shared memory beside the
+// decoders' writes (about 200 KB a tile at 128 bytes a cycle).  A softmax group of 128 rows needs 3600 cycles for
+// 128 scores a thread, two groups in turn.  Beside that a segment begins and ends in 10000 to 14000 cycles (Q, the
+// last product, joining the groups).  Giving raw tiles back before the wait for the operand's place changed nothing.
+// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 209 us for NVFP4
+// (543 TFLOP/s), 302 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
+// each of 16 sequences of 3000 to 4100: 49 us.
 #include <algorithm>
 #include <atomic>
 
@@ -94,7 +97,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
-    int b = plan.b, qt = 0;
+    int b = plan.b, qt = plan.qt;
     Seq s = plan.s;
     uint32_t tiles = 0;
 #pragma unroll 1
@@ -166,6 +169,15 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
                    static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
         };
+        // a later segment's rows of Q, on their way while the last one is worked on
+        for (int r = lane; nseg > 0 && r < rows; r += 32) {
+            const int j = (row0 + r) / a.group;
+            const __nv_bfloat16* src = a.q + static_cast<int64_t>(s.q0 + j) * a.q_token_stride +
+                                  static_cast<int64_t>(head * a.group + row0 + r - j * a.group) * a.q_head_stride;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+            if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+        }
+        __syncwarp();
         int64_t next = source_of(0);
 #pragma unroll 1
         for (int i = 0; i < count; ++i, ++tiles) {
@@ -266,8 +278,9 @@ __device__ __forceinline__ uint32_t largest_code(uint32_t c) {
 
 // Keys of units u, u + 1: a lane has quarter q of token r: 32-bit words of 8 elements, 16 bytes each once
 // decoded.  Eight neighbouring lanes have four tokens and two quarters, whose chunks meet different banks.
-template <int FMT, int D, bool QUAD>
-__device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u, float* factors) {
+// `loaded` is called once the raw bytes are in registers; it waits for the operand's place.
+template <int FMT, int D, bool QUAD, class Loaded>
+__device__ __forceinline__ bool keys(uint32_t raw, uint32_t k16, int u, float* factors, Loaded loaded) {
     using U = typename RCfg<FMT, D, QUAD>::U;
     const int lane = threadIdx.x & 31;
     const int r0 = (lane >> 3 & 1) * 4 + (lane >> 1 & 3), q = (lane >> 4) * 2 + (lane & 1);
@@ -283,6 +296,7 @@ __device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u, float* f
         }
         lds<U::W>(unit + U::k_at(r, q, 0), w[i]);
     }
+    if (!loaded()) return false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t row = u * 16 + 8 * i + r0;
@@ -310,12 +324,13 @@ __device__ __forceinline__ void keys(uint32_t raw, uint32_t k16, int u, float* f
                          make_uint4(hmul2(o[0], f2), hmul2(o[1], f2), hmul2(o[2], f2), hmul2(o[3], f2)));
         }
     }
+    return true;
 }
 
 // Values of unit u, transposed: a lane has tokens 8 h + 2 t, + 1 and channels 16 j + 2 g, + 1.
-template <int FMT, int D, bool QUAD>
+template <int FMT, int D, bool QUAD, class Loaded>
 __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool edge, int pos0, int seen0, int seen1,
-                                       uint8_t* smem, const RowBars& bar, uint32_t n, int (&ref)[4], int* status) {
+                                       uint8_t* smem, const RowBars& bar, uint32_t n, int (&ref)[4], int* status, Loaded loaded) {
     using C = RCfg<FMT, D, QUAD>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -329,6 +344,7 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
         lds<PB>(unit + U::OFF_VS + (t + 4 * h) * PB, sb[h]);
         lds<U::W>(unit + U::OFF_V + h * (4 * D) + lane * U::W, w[h]);
     }
+    if (!loaded()) return false;
     if (edge) {
         // tokens that no row sees: 0, whatever the bytes are; a NaN (the quantizer writes none): the
         // largest number, as 0 times it has to be 0 for the rows that do not see the token
@@ -424,22 +440,25 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
             const uint32_t n = base + i, slot = n % C::STAGES;
             if (!wait_warp(&bar.raw_full[slot], n / C::STAGES & 1u, a.status, 0x5a)) return;
             const uint32_t raw = smem_u32(smem + C::OFF_RAW + slot * C::RAW);
+            // the raw tile is given back as soon as it is in registers, then the operand's place waited for
+            auto loaded = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
+                return warp < kKeyWarps ? wait_warp(&bar.sf[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5b)
+                                        : wait_warp(&bar.od[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5c);
+            };
             if (warp < kKeyWarps) {
-                if (!wait_warp(&bar.sf[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5b)) return;
-                keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp,
-                                   reinterpret_cast<float*>(smem + C::OFF_KF) + (n & 3) * kTokens);
+                if (!keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp,
+                                        reinterpret_cast<float*>(smem + C::OFF_KF) + (n & 3) * kTokens, loaded))
+                    return;
             } else {
-                if (!wait_warp(&bar.od[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5c)) return;
                 if (!values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
-                                          pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status))
+                                          pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status, loaded))
                     return;
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(warp < kKeyWarps ? &bar.kf[n & 1] : &bar.vf[n & 1]);
-                mbar_arrive(&bar.raw_empty[slot]);
-            }
+            if (lane == 0) mbar_arrive(warp < kKeyWarps ? &bar.kf[n & 1] : &bar.vf[n & 1]);
         }
     }
 }
