@@ -304,10 +304,12 @@ size_t mxq_kv_attention_workspace_size(int64_t batch, int64_t max_q, int heads, 
  *                logarithm of the softmax's denominator, or NULL.  A row that sees no token gets zeros and
  *                -inf.  Rows of no sequence are left as they were.
  *   workspace    (device) at least mxq_kv_attention_workspace_size(...) bytes; needs no preparation.
- * fp32 softmax and sums; probabilities are rounded to f16 (11 bits) for the product with V.  MXFP4 blocks
- * of V whose scale is 2^23 or more below the largest in the same 32 channels (over the tokens that one
- * warp takes) count as zero.  Results do not depend on timing.  Two launches.  Calls that may run at the
- * same time need a workspace each.
+ * max_pages * page_size <= 2^30 - 1024.  fp32 softmax and sums; probabilities are rounded to f16 (11 bits)
+ * for the product with V.  MXFP4 blocks of V whose scale is 2^23 or more below the largest in the same 32
+ * channels (over the tokens that are taken together, at most all of the sequence's) count as zero.  Scale
+ * bytes that are not numbers, which the quantizer never writes, have no effect where no row sees the token;
+ * rows that see it, and in MXFP4 their neighbours of the same sequence, get anything.  Results do not
+ * depend on timing.  Two launches.  Calls that may run at the same time need a workspace each.
  */
 int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
                      int64_t num_pages, int page_size, int heads, int kv_heads, int head_dim, mxq_fmt fmt,

@@ -402,6 +402,14 @@ def _on(t):
     return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory of the call's stream: what a freed block still waits for, or is given to next, is on that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _at(t, name, dtype, n, device):
     """Pointer of a contiguous tensor of at least n elements of dtype on the call's device (None passes)."""
     if t is None:
@@ -465,11 +473,11 @@ def kv_read(cache, slots, fmt, head_dim, g_k=None, g_v=None, k_out=None, v_out=N
     pages, H, page_size = _kv_layer(cache, head_dim, f)
     T = slots.numel()
     if k_out is None and v_out is None:  # one allocation
-        k_out, v_out = torch.empty((2, T, H, head_dim), dtype=_BF16, device=dev).unbind(0)
+        k_out, v_out = _empty((2, T, H, head_dim), _BF16, dev, stream).unbind(0)
     elif k_out is None:
-        k_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
+        k_out = _empty((T, H, head_dim), _BF16, dev, stream)
     elif v_out is None:
-        v_out = torch.empty((T, H, head_dim), dtype=_BF16, device=dev)
+        v_out = _empty((T, H, head_dim), _BF16, dev, stream)
     n = T * H * head_dim
     _call("mxq_kv_read", dev, stream, _at(cache, "cache", _U8, 0, dev), pages, page_size, H, head_dim, f, _at(slots, "slots", _I32, T, dev), T,
           _at(g_k, "g_k", _F32, 1, dev), _at(g_v, "g_v", _F32, 1, dev), _at(k_out, "k_out", _BF16, n, dev),
@@ -502,15 +510,15 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     if (t1 != 1 and cols > 1) or block_table.dtype is not _I32 or block_table.device != dev:
         raise MxqBufferError("block_table must be torch.int32 [batch, pages] with contiguous rows, on the call's device")
     if out is None:
-        out = torch.empty((rows, heads, D), dtype=out_dtype, device=dev)
+        out = _empty((rows, heads, D), out_dtype, dev, stream)
     dtype = out.dtype
     if dtype is not _F32 and dtype is not _BF16:
         raise MxqBufferError("out must be torch.bfloat16 or torch.float32 (got %s)" % dtype)
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=_F32, device=dev)
+        lse = _empty((rows, heads), _F32, dev, stream)
     if workspace is None:
         with _on(q):
-            workspace = torch.empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), dtype=_U8, device=dev)
+            workspace = _empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), _U8, dev, stream)
     _call("mxq_kv_attention", dev, stream, qp, rows, qs, qh, _at(cache, "cache", _U8, 0, dev), pages, page_size, heads, kv_heads, D, f,
           block_table.data_ptr(), t0 if batch > 1 else max(cols, 1), cols, _at(kv_lens, "kv_lens", _I32, batch, dev),
           batch, _at(q_start, "q_start", _I32, batch + 1, dev), max_q, D ** -0.5 if scale is None else scale, causal, window,
@@ -520,14 +528,14 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     return out, lse
 
 
-def _pages_args(block_table, kv_lens, refs, info, page_size):
+def _pages_args(block_table, kv_lens, refs, info, page_size, stream):
     """Checks the page state; the arguments that all page calls share, and info."""
     dev = refs.device
     if block_table.dim() != 2 or not block_table.is_contiguous():
         raise MxqBufferError("block_table must be a contiguous [rows, pages] tensor")
     rows, cols = block_table.shape
     if info is None:
-        info = torch.empty(2, dtype=_I32, device=dev)
+        info = _empty(2, _I32, dev, stream)
     return (_at(block_table, "block_table", _I32, 0, dev), rows, cols, cols, _at(kv_lens, "kv_lens", _I32, rows, dev),
             _at(refs, "refs", _I32, 1, dev), refs.numel(), page_size), info
 
@@ -547,11 +555,11 @@ def _kv_layers(cache, page_size, num_pages, dev):
 def kv_reserve(seqs, add, block_table, kv_lens, refs, cache, page_size, slots=None, info=None, workspace=None, stream=None):
     """Room for add[i] more tokens in row seqs[i] (int32 each); `cache` is [pages, ...] or [layers, pages, ...].
     slots receives the new tokens' slots, then -1.  Returns info (int32[2]: status, pages taken)."""
-    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size, stream)
     n, dev = seqs.numel(), refs.device
     layers = _kv_layers(cache, page_size, refs.numel(), dev)
     if workspace is None:
-        workspace = torch.empty(16 + 8 * n, dtype=_U8, device=dev)
+        workspace = _empty(16 + 8 * n, _U8, dev, stream)
     _call("mxq_kv_reserve", dev, stream, _at(seqs, "seqs", _I32, n, dev), _at(add, "add", _I32, n, dev), n, *state, *layers,
           _at(slots, "slots", _I32, 0, dev), 0 if slots is None else slots.numel(), _at(info, "info", _I32, 2, dev),
           _at(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size())
@@ -560,7 +568,7 @@ def kv_reserve(seqs, add, block_table, kv_lens, refs, cache, page_size, slots=No
 
 def kv_fork(parents, children, block_table, kv_lens, refs, page_size, info=None, stream=None):
     """Empty row children[i] becomes a copy of row parents[i] that shares its pages.  Returns info."""
-    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size, stream)
     n, dev = parents.numel(), refs.device
     _call("mxq_kv_fork", dev, stream, _at(parents, "parents", _I32, n, dev), _at(children, "children", _I32, n, dev), n,
           *state, _at(info, "info", _I32, 2, dev))
@@ -569,7 +577,7 @@ def kv_fork(parents, children, block_table, kv_lens, refs, page_size, info=None,
 
 def kv_truncate(seqs, new_lens, block_table, kv_lens, refs, page_size, info=None, stream=None):
     """Cut row seqs[i] to new_lens[i] tokens (0 frees it).  Returns info."""
-    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size, stream)
     n, dev = seqs.numel(), refs.device
     _call("mxq_kv_truncate", dev, stream, _at(seqs, "seqs", _I32, n, dev), _at(new_lens, "new_lens", _I32, n, dev), n, *state,
           _at(info, "info", _I32, 2, dev))
@@ -583,11 +591,11 @@ def kv_compact_workspace(num_pages):
 
 def kv_compact(block_table, kv_lens, refs, cache, page_size, info=None, workspace=None, stream=None):
     """Pack the pages in use to the front of the cache.  Returns info (int32[2]: 0, pages in use)."""
-    state, info = _pages_args(block_table, kv_lens, refs, info, page_size)
+    state, info = _pages_args(block_table, kv_lens, refs, info, page_size, stream)
     dev = refs.device
     layers = _kv_layers(cache, page_size, refs.numel(), dev)
     if workspace is None:
-        workspace = torch.empty(kv_compact_workspace(refs.numel()), dtype=_U8, device=dev)
+        workspace = _empty(kv_compact_workspace(refs.numel()), _U8, dev, stream)
     _call("mxq_kv_compact", dev, stream, *state, *layers, _at(info, "info", _I32, 2, dev),
           _at(workspace, "workspace", workspace.dtype, 0, dev), workspace.numel() * workspace.element_size())
     return info

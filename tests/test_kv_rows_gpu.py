@@ -194,3 +194,47 @@ def test_bad_pages_in_row_tiles_are_reported(orc, fmt, q):
     assert st == 0 and not out[q:].any() and torch.equal(out[:q], good[:q])
     for starts in ([0, q, 2 * q + 1], [-1, q, 2 * q], [0, 2 * q, q], [0, q + 1, 2 * q]):
         assert call(p.table, p.lens, _dev(starts))[1] == 0x202, starts
+
+
+@pytest.mark.parametrize("q", [1, 20, 70])
+def test_memory_of_a_call_on_a_given_stream(orc, q):
+    """What a call allocates for a stream it is given is not handed to the current stream meanwhile."""
+    p = Problem("nvfp4", 128, 8, 1, 64, [3000] * 4, [q] * 4, seed=51)
+    want, _ = p.run()
+    cache, table, lens, qd = torch.from_numpy(p.cache).cuda(), _dev(p.table), _dev(p.lens), p.q.cuda()
+    size = mxq.kv_attention_workspace(4, q, 8, 8, 128)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs, others = [], []
+    for _ in range(30):
+        outs.append(mxq.kv_attention(qd, cache, table, lens, "nvfp4", max_q=q, g_k=p.dk, g_v=p.dv, stream=s)[0])
+        others.append(torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda"))
+        del others[:-1]
+    torch.cuda.synchronize()
+    assert _status() == 0 and all(torch.equal(o, want) for o in outs)
+
+
+def test_pages_and_tokens_on_a_given_stream(orc):
+    """Reserve, append, attention, fork and compaction in a row on a stream that is not the current one."""
+    D, H, page, P = 128, 2, 16, 12
+    s = torch.cuda.Stream()
+    cache = torch.zeros(mxq.kv_cache_shape(P, H, D, "mxfp4", page), dtype=torch.uint8, device="cuda")
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
+    slots = torch.empty(37, dtype=torch.int32, device="cuda")
+    k, v, q = _rand((37, H, D), 1).cuda(), _rand((37, H, D), 2).cuda(), _rand((1, 2 * H, D), 3).cuda()
+    rows = [_dev([i]) for i in range(3)]
+    count, none = _dev([37]), _dev([0])
+    torch.cuda.synchronize()
+    state = (table, lens, refs)
+    infos = [mxq.kv_reserve(rows[1], count, *state, cache, page, slots=slots, stream=s)]
+    mxq.kv_append(k, v, cache, slots, "mxfp4", stream=s)
+    infos.append(mxq.kv_fork(rows[1], rows[2], *state, page, stream=s))
+    infos.append(mxq.kv_truncate(rows[1], none, *state, page, stream=s))
+    infos.append(mxq.kv_compact(*state, cache, page, stream=s))
+    out, lse = mxq.kv_attention(q, cache, table[2:], lens[2:], "mxfp4", stream=s)
+    torch.cuda.synchronize()
+    assert [i.tolist() for i in infos] == [[0, 3], [0, 3], [0, 3], [0, 3]] and _status() == 0
+    ref = kh.attention(q.double().cpu().numpy(), cache.cpu().numpy(), table[2:].cpu().numpy(), [37], [0, 1], "mxfp4",
+                       np.float64(np.float32(D ** -0.5)), True, 0, None, None)
+    kh.check_attention(out, lse, ref, "stream")
