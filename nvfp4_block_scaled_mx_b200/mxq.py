@@ -5,8 +5,8 @@ handle).  The tensor helpers below only allocate outputs with torch and marshal 
 step of the computation runs in the library's kernels.  There is no fallback: if the library is
 missing or the device is not an sm_100 part, the calls raise.
 """
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -397,9 +397,11 @@ def _call(name, device, stream, *args):
         raise MxqError(rc, name)
 
 
-def _on(t):
-    """The device context of a tensor's device, where a size depends on the device."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(index, *sizes):
+    """kv_attention_workspace on device `index` (a function of its arguments alone)."""
+    with torch.cuda.device(index):
+        return max(kv_attention_workspace(*sizes), 16)
 
 
 def _empty(shape, dtype, device, stream):
@@ -517,8 +519,8 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     if lse is None:
         lse = _empty((rows, heads), _F32, dev, stream)
     if workspace is None:
-        with _on(q):
-            workspace = _empty(max(kv_attention_workspace(batch, max_q, heads, kv_heads, D), 16), _U8, dev, stream)
+        size = _attention_bytes(dev.index, batch, max_q, heads, kv_heads, D) if q.is_cuda else 16
+        workspace = _empty(size, _U8, dev, stream)
     _call("mxq_kv_attention", dev, stream, qp, rows, qs, qh, _at(cache, "cache", _U8, 0, dev), pages, page_size, heads, kv_heads, D, f,
           block_table.data_ptr(), t0 if batch > 1 else max(cols, 1), cols, _at(kv_lens, "kv_lens", _I32, batch, dev),
           batch, _at(q_start, "q_start", _I32, batch + 1, dev), max_q, D ** -0.5 if scale is None else scale, causal, window,
