@@ -21,9 +21,8 @@
 // workspace as (m, l, O); a second kernel joins those in CTA order, so results do not depend on timing.
 //
 // What bounds it: beginning (5 us from the dependency to a CTA's first tile: lengths, page numbers and tiles, one
-// round trip each), then the conversions and the instructions around them (three CTAs of an SM take 8.1 tiles
-// of 32 tokens a us, 5.5 TB/s over the GPU; older warps go first, so that equal shares end up to 10 us apart),
-// then the join (5 us).  40 heads, 8 kv heads of 128: one sequence of 131061 (NVFP4, 151 MB) 43.5 us, 32
+// round trip each), then about 5 TB/s of tiles (ALU pipe 50 % busy; the three CTAs of an SM come forward unequally,
+// equal shares end up to 10 us apart), then the join (5 us).  40 heads, 8 kv heads of 128: one sequence of 131061 (NVFP4, 151 MB) 43.5 us, 32
 // sequences of 500 to 16000 (MXFP4, 161 MB) 49.6 us, one of 1009 11.7 us; 24 heads, 4 kv heads of 256, a window
 // of 2048 over 24 sequences of 90 to 9000 (MXFP4, 29 MB) 24.7 us.
 #include <algorithm>

@@ -238,3 +238,29 @@ def test_pages_and_tokens_on_a_given_stream(orc):
     ref = kh.attention(q.double().cpu().numpy(), cache.cpu().numpy(), table[2:].cpu().numpy(), [37], [0, 1], "mxfp4",
                        np.float64(np.float32(D ** -0.5)), True, 0, None, None)
     kh.check_attention(out, lse, ref, "stream")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G,q", [(5, 1), (1, 20), (1, 80)])
+def test_scales_of_zero_and_below(orc, fmt, G, q):
+    p = Problem(fmt, 128, 1, G, 16, [200, 1], [q, 1], seed=61)
+    for scale in (0.0, -0.3):
+        out, lse = p.run(scale=scale, out_dtype=torch.float32)
+        kh.check_attention(out, lse, p.ref(scale=scale), "%s %g" % (fmt, scale))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G,q", [(5, 1), (1, 20), (1, 80)])
+def test_a_query_that_is_not_finite_leaves_the_other_rows(orc, fmt, G, q):
+    p = Problem(fmt, 128, 1, G, 16, [200, 33], [q, 1], seed=62)
+    ref = p.ref()
+    bad = p.q.clone()
+    flat = bad.view(-1, 128)
+    hurt = [1, flat.shape[0] - 1]
+    flat[hurt[0], 7] = float("inf")
+    flat[hurt[1], 9] = float("nan")
+    out, lse = p.run(bad, out_dtype=torch.float32)
+    keep = [i for i in range(flat.shape[0]) if i not in hurt]
+    kh.check_attention(out.view(-1, 1, 128)[keep], lse.view(-1, 1)[keep],
+                       tuple(x.reshape(-1, 1, x.shape[-1])[keep] if x.ndim == 3 else x.reshape(-1, 1)[keep] for x in ref), fmt)
+    assert not torch.isfinite(out.view(-1, 128)[hurt[1]]).any()
