@@ -264,3 +264,40 @@ def test_a_query_that_is_not_finite_leaves_the_other_rows(orc, fmt, G, q):
     kh.check_attention(out.view(-1, 1, 128)[keep], lse.view(-1, 1)[keep],
                        tuple(x.reshape(-1, 1, x.shape[-1])[keep] if x.ndim == 3 else x.reshape(-1, 1)[keep] for x in ref), fmt)
     assert not torch.isfinite(out.view(-1, 128)[hurt[1]]).any()
+
+
+def _guarded(shape, dtype):
+    """A tensor inside an allocation of 0xA5 bytes, 4096 on either side."""
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    raw = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    return raw, raw[4096:4096 + n].view(dtype).view(shape)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,q", [(64, 3, 1), (128, 5, 1), (256, 5, 3), (128, 5, 4), (128, 5, 31), (64, 1, 129), (256, 2, 40)])
+def test_nothing_around_the_outputs_is_written(orc, fmt, D, G, q):
+    p = Problem(fmt, D, 2, G, 16, [700, 0, 33, 1201, 5], [q, q, 1, q, 1], seed=71)
+    rows = int(p.q_start[-1])
+    raws = []
+
+    def guarded(shape, dtype):
+        raw, t = _guarded(shape, dtype)
+        raws.append((raw, t.numel() * t.element_size()))
+        return t
+
+    cache = guarded(p.cache.shape, torch.uint8)
+    cache.zero_()
+    k, v = _rand((p.cache.shape[0] * 16, 2, D), 71), _rand((p.cache.shape[0] * 16, 2, D), 72)
+    slots = torch.arange(k.shape[0], dtype=torch.int32, device="cuda")
+    mxq.kv_append(k.cuda(), v.cuda(), cache, slots, fmt, g_k=p.dk, g_v=p.dv)
+    assert np.array_equal(cache.cpu().numpy(), p.cache)
+    ko, vo = guarded(k.shape, torch.bfloat16), guarded(v.shape, torch.bfloat16)
+    mxq.kv_read(cache, slots, fmt, D, g_k=p.dk, g_v=p.dv, k_out=ko, v_out=vo)
+    out, lse = guarded((rows, 2 * G, D), torch.bfloat16), guarded((rows, 2 * G), torch.float32)
+    ws = guarded((mxq.kv_attention_workspace(5, q, 2 * G, 2, D),), torch.uint8)
+    mxq.kv_attention(p.q.cuda(), cache, _dev(p.table), _dev(p.lens), fmt, q_start=_dev(p.q_start), max_q=q, g_k=p.dk, g_v=p.dv,
+                     out=out, lse=lse, workspace=ws)
+    assert _status() == 0
+    kh.check_attention(out, lse, p.ref(), "guarded")
+    for raw, n in raws:
+        assert (raw[:4096] == 0xA5).all() and (raw[4096 + n:] == 0xA5).all()
