@@ -24,10 +24,11 @@
 // What bounds it: a tile takes 2200 to 2500 cycles.  The products alone take 1750: eight instructions of S and of
 // P V are issued in 870 cycles each, not the 512 of an idle SM, as K, V and Q are read from shared memory beside the
 // decoders' writes (about 200 KB a tile at 128 bytes a cycle).  A softmax group of 128 rows needs 3600 cycles for
-// 128 scores a thread, two groups in turn.  Beside that a segment begins and ends in 10000 to 14000 cycles (Q, the
-// last product, joining the groups).  Giving raw tiles back before the wait for the operand's place changed nothing.
-// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 209 us for NVFP4
-// (543 TFLOP/s), 302 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
+// 128 scores a thread, two groups in turn.  Beside that a segment ends in 5000 to 10000 cycles (the last product,
+// joining the groups); with Q brought by the softmax warps afterwards, not by the value warps meanwhile, a chunk took
+// 209 us, not 198.  Giving raw tiles back before the wait for the operand's place changed nothing.
+// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 198 us for NVFP4
+// (573 TFLOP/s), 281 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
 // each of 16 sequences of 3000 to 4100: 49 us.
 #include <algorithm>
 #include <atomic>
@@ -39,6 +40,7 @@ namespace mxq {
 namespace {
 
 constexpr int kSoftWarps = 8, kKeyWarps = 4, kValueWarps = 8, kDecWarps = kKeyWarps + kValueWarps;
+static_assert(kSoftWarps == 8 && kValueWarps == 8, "either bring Q");
 constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
 constexpr int kRowThreads = (kMmaWarp + 1) * 32;
 constexpr int kTokens = 128;  // of a tile
@@ -61,9 +63,9 @@ struct RCfg {
     static_assert(!QUAD || (FMT == MXQ_NVFP4 && D == 128 && 4 * 32 * MERGE * 4 <= Q16), "what is joined in one CTA");
     static constexpr int OFF_RAW = OFF_Q + Q16;
     static constexpr int OFF_ML = OFF_RAW + STAGES * RAW;  // [2 groups][128 lanes] (base, l)
-    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // scale of each row's scores
+    static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // scale of each row's scores, two buffers
     // MXFP4: of the last four tiles, each token's key factor, and the reference codes and largest codes of V's blocks
-    static constexpr int OFF_KF = OFF_QS + 128 * 4;
+    static constexpr int OFF_KF = OFF_QS + 2 * 128 * 4;
     static constexpr int OFF_REF = OFF_KF + (FMT == MXQ_MXFP4 ? 4 * kTokens * 4 : 0);
     static constexpr int OFF_MAX = OFF_REF + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
     static constexpr int OFF_SEG = OFF_MAX + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
@@ -417,23 +419,91 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
     return true;
 }
 
+template <int FMT>
+__device__ __forceinline__ float score_scale(const KvAttnArgs& a) {
+    float s = a.scale * 1.4426950408889634f;
+    if constexpr (FMT == MXQ_NVFP4) s *= *a.g_k;
+    return s;
+}
+
+// Q rows of a segment: f16 times a power of two (largest element in [2^7, 2^8)).  Of eight warps each takes every
+// eighth row, all its lanes one row at a time; QUAD: the row stands in all four groups of lanes.
+template <int FMT, int D, bool QUAD>
+__device__ __forceinline__ void queries(const KvAttnArgs& a, const Segment& note, uint8_t* smem, float* qs, float qscale, int warp) {
+    using C = RCfg<FMT, D, QUAD>;
+    const int lane = threadIdx.x & 31;
+    constexpr int WARPS = 8, PER = C::ROWS / WARPS, E = D / 32;  // rows of a warp, elements of a lane
+    uint32_t x[PER < 8 ? PER : 8][E / 2];
+#pragma unroll 1
+    for (int k0 = 0; k0 < PER; k0 += 8) {
+#pragma unroll
+        for (int k = 0; k < 8 && k < PER; ++k) {
+            const int rq = (k0 + k) * WARPS + warp, row = note.row0 + rq, j = row / a.group;
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) x[k][i] = 0;
+            if (rq < note.rows) {
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                    a.q + static_cast<int64_t>(note.q0 + j) * a.q_token_stride +
+                    static_cast<int64_t>(note.head * a.group + row - j * a.group) * a.q_head_stride + lane * E);
+                if constexpr (E == 2) {
+                    x[k][0] = *src;
+                } else {
+                    const uint2 y = *reinterpret_cast<const uint2*>(src);
+                    x[k][0] = y.x, x[k][1] = y.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8 && k < PER; ++k) {
+            const int rq = (k0 + k) * WARPS + warp;
+            uint32_t top = 0;  // bf16 magnitudes order like integers
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[k][i] & 0x7FFF7FFFu);
+            const uint32_t ex = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 7, 8u);
+            const float mul = __uint_as_float((261u - ex) << 23);
+            if (lane == 0) qs[rq] = qscale * __uint_as_float((ex - 7u) << 23);
+            const int e = lane * E, c = e / 8;  // first element, its chunk of 8
+#pragma unroll
+            for (int copy = 0; copy < 128 / C::ROWS; ++copy) {
+                const int tr = copy * C::ROWS + rq;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + (c >> 3) * (128 * 128) + tr * 128 +
+                                                            (((c & 7) ^ (tr & 7)) << 4) + e % 8 * 2);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i)
+                    dst[i] = cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // Decodes tiles to f16 operands: warps 0-3 the keys of two units each, warps 4-11 the values of one.
 template <int FMT, int D, bool QUAD>
 __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, int warp) {
     using C = RCfg<FMT, D, QUAD>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31;
+    const float qscale = QUAD ? 0.0f : score_scale<FMT>(a);
 #pragma unroll 1
     for (uint32_t nseg = 0;; ++nseg) {
         const uint32_t buf = nseg & 1u;
         if (!wait_warp(&bar.seg_full[buf], nseg >> 1 & 1u, a.status, 0x59)) return;
-        const Segment& note = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
+        Segment note = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
         const int count = note.count, seen0 = note.seen0, seen1 = note.seen1, all0 = note.all0, all1 = note.all1;
         const uint32_t base = note.base;
         int pos0 = note.pos0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.seg_empty[buf]);
         if (count < 0) return;
+        // The value warps bring Q, beside the end of the segment before: its last scores are done when their
+        // probabilities are written.  (In QUAD mode the softmax warps do, as their join lies where Q does.)
+        if (!QUAD && warp >= kKeyWarps) {
+            const uint32_t last = base - 1;
+            if (nseg > 0 && !wait_warp(&bar.pf[last & 1], last >> 1 & 1u, a.status, 0x65)) return;
+            queries<FMT, D, QUAD>(a, note, smem, reinterpret_cast<float*>(smem + C::OFF_QS) + buf * 128, qscale, warp - kKeyWarps);
+            if (lane == 0) mbar_arrive(bar.qf);
+        }
         int ref[4] = {-1000, -1000, -1000, -1000};  // MXFP4: E8M0 codes that stand for 2^9 in V's factors
 #pragma unroll 1
         for (int i = 0; i < count; ++i, pos0 += kTokens) {
@@ -480,10 +550,9 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
     const int chunk0 = QUAD ? quad : 0;
     float* merge = reinterpret_cast<float*>(smem + C::OFF_Q);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     float* partials = a.partial + gridDim.x * (sizeof(Split) / 4);
-    float qscale = a.scale * 1.4426950408889634f, gv = 1.0f;
-    if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k, gv = *a.g_v;
+    const float gv = FMT == MXQ_NVFP4 ? *a.g_v : 1.0f;
+    const float qscale = QUAD ? score_scale<FMT>(a) : 0.0f;
     uint32_t v[32];
 #pragma unroll 1
     for (uint32_t nseg = 0;; ++nseg) {
@@ -495,55 +564,13 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.seg_empty[buf]);
         if (note.count < 0) return;
-        // Q rows: f16 times a power of two (largest element in [2^7, 2^8)).  A warp takes every eighth row,
-        // all its lanes one row at a time; QUAD: the row stands in all four groups of lanes.
-        {
-            constexpr int PER = C::ROWS / kSoftWarps, E = D / 32;  // rows of a warp, elements of a lane
-            uint32_t x[PER < 8 ? PER : 8][E / 2];
-#pragma unroll 1
-            for (int k0 = 0; k0 < PER; k0 += 8) {
-#pragma unroll
-                for (int k = 0; k < 8 && k < PER; ++k) {
-                    const int rq = (k0 + k) * kSoftWarps + warp, row = note.row0 + rq, j = row / a.group;
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) x[k][i] = 0;
-                    if (rq < note.rows) {
-                        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                            a.q + static_cast<int64_t>(note.q0 + j) * a.q_token_stride +
-                            static_cast<int64_t>(note.head * a.group + row - j * a.group) * a.q_head_stride + lane * E);
-                        if constexpr (E == 2) {
-                            x[k][0] = *src;
-                        } else {
-                            const uint2 y = *reinterpret_cast<const uint2*>(src);
-                            x[k][0] = y.x, x[k][1] = y.y;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 8 && k < PER; ++k) {
-                    const int rq = (k0 + k) * kSoftWarps + warp;
-                    uint32_t top = 0;  // bf16 magnitudes order like integers
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[k][i] & 0x7FFF7FFFu);
-                    const uint32_t ex = max(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)) >> 7, 8u);
-                    const float mul = __uint_as_float((261u - ex) << 23);
-                    if (lane == 0) qs[rq] = qscale * __uint_as_float((ex - 7u) << 23);
-                    const int e = lane * E, c = e / 8;  // first element, its chunk of 8
-#pragma unroll
-                    for (int copy = 0; copy < 128 / C::ROWS; ++copy) {
-                        const int tr = copy * C::ROWS + rq;
-                        uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + (c >> 3) * (128 * 128) + tr * 128 +
-                                                                    (((c & 7) ^ (tr & 7)) << 4) + e % 8 * 2);
-#pragma unroll
-                        for (int i = 0; i < E / 2; ++i)
-                            dst[i] = cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
-                    }
-                }
-            }
+        float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + buf * 128;
+        if constexpr (QUAD) {
+            queries<FMT, D, QUAD>(a, note, smem, qs, qscale, warp);
+            if (lane == 0) mbar_arrive(bar.qf);
+        } else {
+            dead = !wait_warp(bar.qf, nseg & 1u, a.status, 0x64);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.qf);
         // this thread's row
         int first = 0, end = 0;
         const bool real = r < note.rows;
@@ -554,7 +581,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
             s.kv = note.kv, s.q0 = note.q0, s.qn = note.qn;
             if (real) row_span(a, s, row, first, end);
         }
-        named_barrier_sync(1, kSoftWarps * 32);
+        if (named_barrier_or(1, kSoftWarps * 32, dead)) return;
         const float cs = qs[r];
 
         float base = kNegMax, l = 0.0f;
@@ -826,7 +853,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) kv_attention_rows_kernel(const
             mbar_init(&bar.seg_full[i], 1);
             mbar_init(&bar.seg_empty[i], kSoftWarps + kDecWarps + 1);
         }
-        mbar_init(bar.qf, kSoftWarps);
+        mbar_init(bar.qf, 8);  // softmax warps or value warps
         fence_barrier_init();
     }
     if (FMT == MXQ_MXFP4 && threadIdx.x < 16) reinterpret_cast<int*>(smem + C::OFF_MAX)[threadIdx.x] = 0;
