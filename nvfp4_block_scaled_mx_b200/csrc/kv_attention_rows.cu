@@ -26,10 +26,10 @@
 // decoders' writes (about 200 KB a tile at 128 bytes a cycle).  A softmax group of 128 rows needs 3600 cycles for
 // 128 scores a thread, two groups in turn.  Beside that a segment ends in 5000 to 10000 cycles (the last product,
 // joining the groups); with Q brought by the softmax warps afterwards, not by the value warps meanwhile, a chunk took
-// 209 us, not 198.  Giving raw tiles back before the wait for the operand's place changed nothing.
-// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 198 us for NVFP4
-// (573 TFLOP/s), 281 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
-// each of 16 sequences of 3000 to 4100: 49 us.
+// 11 us more.  Giving raw tiles back before the wait for the operand's place changed nothing.
+// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 195 us for NVFP4
+// (582 TFLOP/s), 279 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
+// each of 16 sequences of 3000 to 4100: 48 us.
 #include <algorithm>
 #include <atomic>
 
@@ -45,13 +45,15 @@ constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
 constexpr int kRowThreads = (kMmaWarp + 1) * 32;
 constexpr int kTokens = 128;  // of a tile
 constexpr int kMinRowTiles = 2;
-constexpr int kExtraRowTiles = 8;  // counted for beginning a row tile (a chunk of 700: 229 us at 0, 226 at 4, 219 at 8)
 constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^7; above 2^15 it is raised
 
 template <int FMT, int D, bool QUAD>
 struct RCfg {
     using U = KvUnit<FMT, D>;
     static constexpr int ROWS = QUAD ? 32 : 128;
+    // Tiles counted for beginning a row tile: a chunk of 700 takes 196 us at 3, 195 at 5, 198 at 8, 206 at 12; four drafted
+    // tokens 48.8 at 5, 48.7 at 8, 48.3 at 12, 49.4 at 16.
+    static constexpr int EXTRA = QUAD ? 12 : 5;
     static constexpr int UNITS = kTokens / 16;
     static constexpr int RAW = UNITS * U::BYTES;
     static constexpr int STAGES = 3;
@@ -95,7 +97,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
     using C = RCfg<FMT, D, QUAD>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31;
-    const Plan plan = make_plan<kTokens, C::ROWS, kExtraRowTiles>(a, kMinRowTiles);
+    const Plan plan = make_plan<kTokens, C::ROWS, C::EXTRA>(a, kMinRowTiles);
     if (lane == 0) reinterpret_cast<Split*>(a.partial)[blockIdx.x].parts = 0;
     int64_t at = plan.at, off = plan.off;
     const int64_t stop = min(at + plan.per, plan.work);
@@ -118,7 +120,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             }
             const TileSpan span = tile_span<kTokens, C::ROWS>(a, s.kv, s.qn, qt);
             t0 = span.first, n = span.count;
-            const int64_t each = n + kExtraRowTiles;  // of a head
+            const int64_t each = n + C::EXTRA;  // of a head
             if (off >= each * a.kv_heads) {
                 off -= each * a.kv_heads;
                 ++qt;
@@ -126,8 +128,8 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             }
             head = div_small(off, each, place);
             share = min(each - place, stop - at);
-            from = max(static_cast<int>(place) - kExtraRowTiles, 0);
-            count = max(static_cast<int>(place + share) - kExtraRowTiles, 0) - from;
+            from = max(static_cast<int>(place) - C::EXTRA, 0);
+            count = max(static_cast<int>(place + share) - C::EXTRA, 0) - from;
             if (count > 0) break;
             at += share;  // nothing but tiles that are only counted
             off += share;
@@ -154,7 +156,7 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             note->begins = from == 0;
             note->whole = from == 0 && count == n;
             int64_t rest;
-            note->parts = from == 0 ? div_small(at - place + kExtraRowTiles + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
+            note->parts = from == 0 ? div_small(at - place + C::EXTRA + n - 1, plan.per, rest) - static_cast<int>(blockIdx.x) + 1 : 0;
             mbar_arrive(&bar.seg_full[buf]);
         }
         const int first_unit = (t0 + from) * C::UNITS;
