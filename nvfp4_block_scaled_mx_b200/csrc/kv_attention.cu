@@ -751,18 +751,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 
 // --------------------------------------------------------------------------------------- host
 
-// n-tiles of eight rows a CTA takes at once, one or two: the second one costs 8/9 of the first (its K and V are
-// decoded already), but the last row tile pads to 16 rows (head size 256, 20 rows: 100 us with one, 118 with
-// two; 10 rows: 71 and 66; 500 rows: 1814 and 1618).  Three or four leave room for half the warps (MXFP4, a chunk
-// of 700 tokens: 772 us with two, 855 and 817 with three and four).
-int n_tiles(int64_t rows) { return 9 * ((rows + 7) / 8) < 16 * ((rows + 15) / 16) ? 1 : 2; }
+// n-tiles of eight rows a CTA takes at once, one or two: the second one costs 3/4 of the first (head size 256: 8/9), as
+// K and V are decoded already, but the last row tile pads to 16 rows.  Head size 128, NVFP4: 20 rows 55 us with
+// one, 54 with two; 35 rows 82 and 75; head size 256: 10 rows 71 and 66, 20 rows 100 and 118, 500 rows 1814 and
+// 1618.  Three or four leave room for half the warps (MXFP4, a chunk of 700 tokens: 772 us with two, 855 and 817).
+int n_tiles(int64_t rows, int D) {
+    const int64_t ones = (rows + 7) / 8, twos = 2 * ((rows + 15) / 16);
+    return (D == 256 ? 9 * ones < 8 * twos : ones == 1) ? 1 : 2;
+}
 
 // Rows from which a row tile on tcgen05 (32 rows for NVFP4 with head size 128, else 128) takes less time.  16
 // sequences of 3000 to 4100, 8 kv heads, here and there, in us: NVFP4, 128 wide, 10 rows 35 and 47, 20 rows 54 and
-// 48, 65 rows 115 and 77; 64 wide, 35 rows 50 and 61, 65 rows 73 and 62; MXFP4, 128 wide, 35 rows 79 and 103, 65 rows
-// 122 and 106, 500 rows 688 and 339; 64 wide, 65 rows 76 and 82, 500 rows 402 and 262.
+// 48, 65 rows 115 and 75; 64 wide, 35 rows 50 and 61, 65 rows 73 and 62; MXFP4, 128 wide, 35 rows 79 and 99, 65 rows
+// 122 and 101, 500 rows 688 and 302; 64 wide, 35 rows 51 and 75, 65 rows 76 and 76, 500 rows 402 and 231.
 bool on_tcgen05(int fmt, int D, int64_t rows) {
-    return D <= 128 && rows > (fmt == MXQ_NVFP4 && D == 128 ? 16 : 64);
+    return D <= 128 && rows > (fmt == MXQ_NVFP4 && D == 128 ? 16 : 48);
 }
 
 constexpr int kMaxCtasPerSm = 4;
@@ -815,7 +818,7 @@ int run_dim(int D, int nt, KvAttnArgs& a, cudaStream_t st) {
 size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_heads, int D) {
     (void)batch;
     const int64_t rows = max_q * (heads / kv_heads);
-    const size_t here = static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * 8 * n_tiles(rows) * (D + 2) * 4 + sizeof(Split));
+    const size_t here = static_cast<size_t>(sm_count()) * kMaxCtasPerSm * (2 * 8 * n_tiles(rows, D) * (D + 2) * 4 + sizeof(Split));
     const size_t there = static_cast<size_t>(sm_count()) * (2 * kv_rows_tile(rows) * (D + 2) * 4 + sizeof(Split));
     return rows > 16 && D <= 128 ? std::max(here, there) : here;
 }
@@ -823,7 +826,7 @@ size_t kv_attention_workspace(int64_t batch, int64_t max_q, int heads, int kv_he
 int launch_kv_attention(int fmt, int D, KvAttnArgs& a, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.max_q) * a.group;
     if (on_tcgen05(fmt, D, rows)) return launch_kv_attention_rows(fmt, D, a, st);
-    const int nt = n_tiles(rows);
+    const int nt = n_tiles(rows, D);
     return fmt == MXQ_NVFP4 ? run_dim<MXQ_NVFP4>(D, nt, a, st) : run_dim<MXQ_MXFP4>(D, nt, a, st);
 }
 
