@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr int CTAS = NT * KS <= 8 ? 3 : NT * KS <= 24 ? 2 : 1;
     static constexpr int BUDGET = (227 / CTAS - 1) * 1024 - 1024;
     static constexpr int FIXED = 2 * Q_BYTES + RED + 2 * (ROWS * 12 + 64) + kWarps * ROWS * 8 + 64;
-    static constexpr int FIT = (BUDGET - FIXED) / (TILE_BYTES + 16);
+    static constexpr int FIT = (BUDGET - FIXED) / (TILE_BYTES + 20);
     // A multiple of kWarps: tile n goes to warp n % kWarps, so that a slot's uses are all of one warp, in turn.
     // (Were they not, a warp could wait for use c of a slot whose use c - 1, another warp's, has not landed: the
     // barrier's one parity bit would let it pass.)
@@ -67,7 +67,8 @@ struct Cfg {
     static constexpr int OFF_SEG = OFF_ROW + 2 * ROWS * 12;
     static constexpr int OFF_ML = OFF_SEG + 2 * 64;
     static constexpr int OFF_BAR = OFF_ML + kWarps * ROWS * 8;  // full, empty, segment full, segment empty
-    static constexpr int BYTES = OFF_BAR + (2 * STAGES + 4) * 8;
+    static constexpr int OFF_SKIP = OFF_BAR + (2 * STAGES + 4) * 8;  // of each slot, a bit for each unit of a page outside the cache
+    static constexpr int BYTES = OFF_SKIP + STAGES * 4;
     static_assert(sizeof(Segment) <= 64, "segment note");
     static constexpr float SHIFT = FMT == MXQ_NVFP4 ? 7.0f : 4.0f;  // log2 of what P is multiplied by
 };
@@ -200,11 +201,11 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
 }
 
 // One token tile: scores, softmax update, O update.  pos0 is the tile's first token; MASK: some row does
-// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees.  (One copy of the code
+// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees; skip: units that no row sees.  (One copy of the code
 // with branches in it took 75 us where the two take 65: the branches part what the scheduler interleaves.)
 template <int FMT, int D, int NT, bool MASK>
 __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, uint32_t qf, const float (&cs)[NT][2],
-                                          const int* row_first, const int* row_end, int pos0, int seen0, int seen1) {
+                                          const int* row_first, const int* row_end, int pos0, int seen0, int seen1, uint32_t skip) {
     using C = Cfg<FMT, D, NT>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -216,7 +217,7 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
         float v = fmaf(s[u][n][i], cs[n][i & 1], -base);
         if constexpr (MASK) {
             const int pos = pos0 + 16 * u + 8 * (i >> 1) + g, r = 8 * n + 2 * t + (i & 1);
-            if (pos < row_first[r] || pos >= row_end[r]) v = __int_as_float(0xff800000);
+            if (pos < row_first[r] || pos >= row_end[r] || (skip >> u & 1u)) v = __int_as_float(0xff800000);
         }
         return v;
     };
@@ -299,7 +300,7 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
             const int pos = pos0 + 16 * u + 2 * t;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t live = pair_mask(pos + 8 * h, seen0, seen1);
+                const uint32_t live = skip >> u & 1u ? 0u : pair_mask(pos + 8 * h, seen0, seen1);
 #pragma unroll
                 for (int i = 0; i < PB / 4; ++i) {
                     sb[h][i] &= live;
@@ -511,12 +512,14 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
 #pragma unroll 1
             for (; issued < limit; issued += BATCH) {
                 int64_t src[C::TU];
+                uint32_t skip = 0;
 #pragma unroll
                 for (int u = 0; u < C::TU; ++u) {
                     src[u] = -1;
                     if (in_page[u] < 0) continue;
                     if (page[u] < 0 || page[u] >= a.num_pages) {
                         kv_status(a.status, kStatusKvPage);
+                        skip |= 1u << u;
                         continue;
                     }
                     src[u] = (static_cast<int64_t>(page[u]) * a.kv_heads + head) * a.page_bytes +
@@ -531,6 +534,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
                     if (todo && mbar_test_wait(&empty[slot], parity)) {
                         todo = false;
                         uint8_t* dst = smem + C::OFF_RING + slot * C::TILE_BYTES;
+                        reinterpret_cast<uint32_t*>(smem + C::OFF_SKIP)[slot] = skip;  // (in front of the arrival below)
                         uint32_t bytes = 0;
 #pragma unroll
                         for (int u = 0; u < C::TU; ++u) bytes += src[u] < 0 ? 0 : U::BYTES;
@@ -666,10 +670,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
                 break;
             }
             const uint32_t tile = smem_u32(smem + C::OFF_RING + slot * C::TILE_BYTES);
-            if (pos0 >= all0 && pos0 + C::TILE <= all1)
-                tile_step<FMT, D, NT, false>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1);
+            const uint32_t skip = reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[slot];
+            if (skip == 0 && pos0 >= all0 && pos0 + C::TILE <= all1)
+                tile_step<FMT, D, NT, false>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, 0);
             else
-                tile_step<FMT, D, NT, true>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1);
+                tile_step<FMT, D, NT, true>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, skip);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }

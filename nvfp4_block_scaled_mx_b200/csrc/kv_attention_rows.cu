@@ -70,7 +70,10 @@ struct RCfg {
     static constexpr int OFF_KF = OFF_QS + 2 * 128 * 4;
     static constexpr int OFF_REF = OFF_KF + (FMT == MXQ_MXFP4 ? 4 * kTokens * 4 : 0);
     static constexpr int OFF_MAX = OFF_REF + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
-    static constexpr int OFF_SEG = OFF_MAX + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
+    // of the last eight tiles, a bit for each unit of a page outside the cache (a tile is eight behind only when its
+    // softmax is done: it is decoded before the third tile behind it is fed, the second's V waits for its product)
+    static constexpr int OFF_SKIP = OFF_MAX + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
+    static constexpr int OFF_SEG = OFF_SKIP + 8 * 4;
     static constexpr int OFF_BAR = OFF_SEG + 2 * 64;
     static constexpr int NBARS = 2 * STAGES + 12 + 1 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
@@ -90,6 +93,12 @@ struct RowBars {
         seg_full = b, seg_empty = b + 2;
     }
 };
+
+// Units of tile n that no row sees, as the feeding warp noted them.
+template <class C>
+__device__ __forceinline__ uint32_t skipped(const uint8_t* smem, uint32_t n) {
+    return reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[n & 7];
+}
 
 // Feeds raw tiles (whole warp): eight lanes have a unit each; neighbouring units of a page go as one copy.
 template <int FMT, int D, bool QUAD>
@@ -161,14 +170,14 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
         }
         const int first_unit = (t0 + from) * C::UNITS;
         const int units_end = min((seen1 + 15) >> 4, first_unit + count * C::UNITS);  // behind the tokens pages may not exist
-        auto source_of = [&](int i) -> int64_t {  // of the lane's unit of tile i, -1: not loaded
+        auto source_of = [&](int i) -> int64_t {  // of the lane's unit of tile i; not loaded: -1, and -2 where the page is none of the cache's
             const int unit = first_unit + i * C::UNITS + lane;
             if (lane >= C::UNITS || unit >= units_end) return -1;
             const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));
             const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             if (pg < 0 || pg >= a.num_pages) {
                 kv_status(a.status, kStatusKvPage);
-                return -1;
+                return -2;
             }
             return (static_cast<int64_t>(pg) * a.kv_heads + head) * a.page_bytes +
                    static_cast<int64_t>(unit - at_page * a.page_units) * U::BYTES;
@@ -189,11 +198,14 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             next = source_of(i + 1);
             const uint32_t slot = tiles % C::STAGES;
             if (!wait_warp(&bar.raw_empty[slot], (tiles / C::STAGES & 1u) ^ 1u, a.status, 0x52)) return;
-            const uint32_t valid = __ballot_sync(0xffffffffu, src >= 0);
+            const uint32_t valid = __ballot_sync(0xffffffffu, src >= 0), skip = __ballot_sync(0xffffffffu, src == -2);
             const int64_t before = __shfl_up_sync(0xffffffffu, src, 1);
             const bool cont = lane > 0 && src >= 0 && before >= 0 && src == before + U::BYTES;
             const uint32_t conts = __ballot_sync(0xffffffffu, cont);
-            if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[slot], __popc(valid) * U::BYTES);
+            if (lane == 0) {
+                reinterpret_cast<uint32_t*>(smem + C::OFF_SKIP)[tiles & 7] = skip;  // (in front of the arrival)
+                mbar_arrive_expect_tx(&bar.raw_full[slot], __popc(valid) * U::BYTES);
+            }
             __syncwarp();
             if (src >= 0 && !cont) {
                 const int run = __ffs(~(conts >> (lane + 1)));  // this unit and those that follow it without a gap
@@ -256,7 +268,7 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
                                  smem_desc(k + at, 16, 1024, kLayoutSwizzle128B), IDESC_S, j == 0 ? 0u : 1u);
                     }
                     tc_commit(&bar.sf[t & 1]);
-                    if constexpr (FMT == MXQ_MXFP4) mbar_arrive(&bar.sf[t & 1]);  // hands the keys' factors on
+                    mbar_arrive(&bar.sf[t & 1]);  // hands on what the feeding and the key warps noted of the tile
                 }
                 __syncwarp();
             }
@@ -352,9 +364,10 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
     if (edge) {
         // tokens that no row sees: 0, whatever the bytes are; a NaN (the quantizer writes none): the
         // largest number, as 0 times it has to be 0 for the rows that do not see the token
+        const uint32_t skip = skipped<C>(smem, n);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t live = pair_mask(pos0 + 16 * u + 8 * h + 2 * t, seen0, seen1);
+            const uint32_t live = skip >> u & 1u ? 0u : pair_mask(pos0 + 16 * u + 8 * h + 2 * t, seen0, seen1);
 #pragma unroll
             for (int i = 0; i < PB / 4; ++i) {
                 sb[h][i] &= live;
@@ -525,7 +538,7 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
                     return;
             } else {
                 if (!values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
-                                          pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status, loaded))
+                                          skipped<C>(smem, n) != 0 || pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status, loaded))
                     return;
             }
             fence_proxy_async_smem();
@@ -601,7 +614,7 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
             const float* kfac = reinterpret_cast<const float*>(smem + C::OFF_KF) + (n & 3) * kTokens;
             const uint32_t s_at = lanes + C::S_COL + group * 128;
             const int pos0 = note.pos0 + static_cast<int>(n - note.base) * kTokens;
-            const bool edge = pos0 < note.all0 || pos0 + kTokens > note.all1;
+            const bool edge = skipped<C>(smem, n) != 0 || pos0 < note.all0 || pos0 + kTokens > note.all1;
 #pragma unroll 1
             for (int c = chunk0; c < chunk0 + CHUNKS; ++c) {
                 auto exponents = [&](float from) {  // of the chunk, relative to `from`; the largest
@@ -625,6 +638,12 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                         for (int k = 0; k < 32; ++k) {
                             const int pos = pos0 + 32 * c + k;
                             if (pos < first || pos >= end) v[k] = 0xff800000u;
+                        }
+                        const uint32_t skip = skipped<C>(smem, n) >> (2 * c);
+                        if (skip & 3u) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (skip >> (k / 16) & 1u) v[k] = 0xff800000u;
                         }
                     }
 #pragma unroll
@@ -848,7 +867,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) kv_attention_rows_kernel(const
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.kf[i], kKeyWarps);
             mbar_init(&bar.vf[i], kValueWarps);
-            mbar_init(&bar.sf[i], FMT == MXQ_MXFP4 ? 2 : 1);
+            mbar_init(&bar.sf[i], 2);  // the products' end, and the issuing lane
             mbar_init(&bar.pf[i], kSoftWarps / 2);
             mbar_init(&bar.od[i], 1);
             mbar_init(&bar.vm[i], kValueWarps);

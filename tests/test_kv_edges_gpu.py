@@ -1,0 +1,72 @@
+"""Calls at the edge of what the key/value cache's documentation allows: pages outside the cache, windows and scores of
+any size, values of very different scale, page calls that name nothing, and arguments left at their defaults."""
+import numpy as np
+import pytest
+import torch
+
+import kv_helpers as kh
+from test_kv_cache_gpu import FMTS, Problem, _rand, _status
+from test_kv_rows_gpu import _dev, _rewrite
+
+from nvfp4_block_scaled_mx_b200 import mxq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def orc():
+    import oracle
+
+    oracle.build()
+    return oracle
+
+
+def _reference(p, hidden, scale=None, causal=True, window=0):
+    """kh.attention's results where the tokens hidden[b] of sequence b are seen by no row."""
+    scale = np.float64(np.float32(p.D ** -0.5 if scale is None else scale))
+    q = p.q.double().numpy()
+    T, Hq, D = q.shape
+    out, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
+    absv, mass, floor = np.zeros((T, Hq, D)), np.zeros((T, Hq)), np.zeros((T, Hq, 1))
+    for b, n in enumerate(p.lens):
+        table = np.where((p.table[b] >= 0) & (p.table[b] < p.cache.shape[0]), p.table[b], 0)
+        k, v = kh.tokens(p.cache, table, n, D, p.fmt, p.gk, p.gv)
+        shown = np.ones(n, bool)
+        shown[list(hidden.get(b, []))] = False
+        rows = range(p.q_start[b], p.q_start[b + 1])
+        for i in rows:
+            seen = n - len(rows) + (i - rows[0]) + 1
+            span = np.arange(n)
+            at = np.flatnonzero(shown & (span < (seen if causal else n)) & (span >= (seen - window if window else 0)))
+            for h in range(Hq):
+                out[i, h], lse[i, h] = 0, -np.inf
+                if len(at):
+                    kk, vv = k[at, h // p.G], v[at, h // p.G]
+                    x = kk @ q[i, h] * scale
+                    e = np.exp(x - x.max())
+                    out[i, h], lse[i, h] = e @ vv / e.sum(), x.max() + np.log(e.sum())
+                    absv[i, h], floor[i, h] = e @ np.abs(vv) / e.sum(), len(vv) * np.abs(vv).max()
+                    mass[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * abs(scale)
+    return out, lse, absv, mass, floor
+
+
+# rows of a sequence and heads that take each kernel and its row tiles
+SHAPES = [(64, 1, 3), (128, 5, 1), (128, 5, 2), (256, 2, 2), (256, 5, 4), (128, 1, 20), (128, 5, 11), (64, 5, 20), (128, 1, 150)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,q", SHAPES)
+@pytest.mark.parametrize("page", [16, 48])
+def test_tokens_of_pages_outside_the_cache_are_skipped(orc, fmt, D, G, q, page):
+    p = Problem(fmt, D, 2, G, page, [301, 200, 37, 150], [q, q, 1, q], seed=q + D)
+    P = p.cache.shape[0]
+    p.table[0, [1, 4]] = P, -1
+    p.table[1, 0] = 2 ** 31 - 1
+    p.table[2, :-(-37 // page)] = -3
+    hidden = {b: [t for t in range(n) if not 0 <= p.table[b, t // page] < P] for b, n in enumerate(p.lens)}
+    cache, qd = torch.from_numpy(p.cache).cuda(), p.q.cuda()
+    for causal, window in ((True, 0), (False, 0), (True, 170)):
+        out, lse = mxq.kv_attention(qd, cache, _dev(p.table), _dev(p.lens), fmt, q_start=_dev(p.q_start), max_q=p.max_q,
+                                    causal=causal, window=window, g_k=p.dk, g_v=p.dv)
+        assert _status() == 0x201
+        kh.check_attention(out, lse, _reference(p, hidden, causal=causal, window=window), "%s %s %d" % (fmt, causal, window))
