@@ -205,7 +205,9 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
     a.num_pages = static_cast<int>(num_pages);
     a.max_len = static_cast<int>(max_pages * page_size);
     a.causal = causal != 0;
-    a.window = static_cast<int>(window);
+    // No sequence is longer than 2^30, so a wider window is no other; a row's own place may be negative, down to
+    // -2^28 (fewer cached tokens than query rows), and the kernels subtract the window from it in 32 bits.
+    a.window = static_cast<int>(window < (int64_t(1) << 30) ? window : int64_t(1) << 30);
     a.out_f32 = out_type == MXQ_OUT_FP32;
     a.scale = scale;
     a.status = status_ptr();

@@ -70,3 +70,16 @@ def test_tokens_of_pages_outside_the_cache_are_skipped(orc, fmt, D, G, q, page):
                                     causal=causal, window=window, g_k=p.dk, g_v=p.dv)
         assert _status() == 0x201
         kh.check_attention(out, lse, _reference(p, hidden, causal=causal, window=window), "%s %s %d" % (fmt, causal, window))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,q", [(64, 1, 9), (128, 1, 9), (256, 1, 9), (128, 2, 30), (64, 4, 40)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_window_wider_than_any_sequence(orc, fmt, D, G, q, causal):
+    # more query tokens than cached ones: the first rows' own places lie in front of the first token
+    p = Problem(fmt, D, 2, G, 16, [5, 300, 0, 70], [q, q, q, 1], seed=D + q)
+    want = p.run(causal=causal)
+    kh.check_attention(*want, p.ref(causal=causal), "no window")
+    for window in (2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30, 400):
+        out, lse = p.run(causal=causal, window=window)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), window
