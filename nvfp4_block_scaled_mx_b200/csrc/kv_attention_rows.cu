@@ -655,7 +655,9 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 };
                 const float m = exponents(base);
                 if (__any_sync(0xffffffffu, m > kLimit)) {
-                    // the product before the last of this group's tiles is done (its S was issued behind it)
+                    // the product before the last of this group's tiles is done (its S was issued behind it); the tile's
+                    // earlier P, which is read back below, is on its way: stores and loads of TMEM are not ordered
+                    tmem_st_wait();
                     const float raw = exponents(0.0f);
                     const float to = m > kLimit ? fmaxf(base, raw - kStart) : base, al = ex2(base - to);
                     base = to;

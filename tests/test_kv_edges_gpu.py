@@ -83,3 +83,37 @@ def test_a_window_wider_than_any_sequence(orc, fmt, D, G, q, causal):
     for window in (2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30, 400):
         out, lse = p.run(causal=causal, window=window)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), window
+
+
+def _levels(fmt, D, q, levels, seed):
+    """One sequence of 700 tokens whose scores rise in steps of 32 tokens, by other amounts in each row, in units of
+    log 2; tokens of step s have values in channel s % 32 (and s % 32 + 32) alone, so that each step's weight shows."""
+    n = 700
+    p = Problem(fmt, D, 1, 1, 16, [n], [q], seed=seed)
+    step = np.minimum(np.arange(n) // 32, len(levels) - 1)
+    k, v = torch.zeros((n, 1, D), dtype=torch.bfloat16), torch.zeros((n, 1, D), dtype=torch.bfloat16)
+    k[:, 0, 0] = torch.tensor(levels, dtype=torch.bfloat16)[step]
+    for c in (0, 32):
+        v[np.arange(n), 0, step % 32 + c] = 1.0
+    if fmt == "nvfp4":
+        p.gk, p.gv = np.float32(1 / 64), np.float32(1 / 64)
+        p.dk, p.dv = torch.tensor([p.gk], device="cuda"), torch.tensor([p.gv], device="cuda")
+    _rewrite(p, k, v)
+    p.q.zero_()
+    p.q[:, 0, 0] = (0.9 + 0.2 * torch.arange(q) / q).to(torch.bfloat16)
+    return p
+
+
+LN2 = float(np.float32(np.log(2.0)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q", [20, 150])
+@pytest.mark.parametrize("up", [9, 12, 24])
+def test_a_maximum_that_rises_inside_a_tile(orc, fmt, D, q, up):
+    """The probabilities of a tile's first tokens are written before a later one raises the row's base."""
+    p = _levels(fmt, D, q, [-up, -up / 2, up / 2, up] + [up - 3] * 4 + [up + 9, 2 * up + 9, 0, 2 * up + 30], seed=q)
+    for causal in (True, False):
+        out, lse = p.run(scale=LN2, causal=causal, out_dtype=torch.float32)
+        kh.check_attention(out, lse, p.ref(scale=LN2, causal=causal), "%s D%d q%d" % (fmt, D, q))
