@@ -45,7 +45,7 @@ constexpr int kFeedWarp = kSoftWarps + kDecWarps, kMmaWarp = kFeedWarp + 1;
 constexpr int kRowThreads = (kMmaWarp + 1) * 32;
 constexpr int kTokens = 128;  // of a tile
 constexpr int kMinRowTiles = 2;
-constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^7; above 2^15 it is raised
+constexpr float kStart = 7.0f, kLimit = 15.0f;  // a fresh base puts the maximum at 2^6 to 2^7; above 2^15 it is raised
 
 template <int FMT, int D, bool QUAD>
 struct RCfg {
@@ -659,7 +659,10 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     // earlier P, which is read back below, is on its way: stores and loads of TMEM are not ordered
                     tmem_st_wait();
                     const float raw = exponents(0.0f);
-                    const float to = m > kLimit ? fmaxf(base, raw - kStart) : base, al = ex2(base - to);
+                    // Bases are whole numbers, so that what is written already changes by a power of two, exactly, in
+                    // l, O and P alike.  (A base at its start is far below; one that is no number makes the row none.)
+                    const float to = m > kLimit ? fmaxf(base, ceilf(raw - kStart)) : base, by = to - base;
+                    const float al = by < 126.0f ? __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(by)) << 23) : 0.0f;
                     base = to;
                     l *= al;
                     if (begun) {
@@ -673,14 +676,16 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                             tmem_st_x16(o_at + k0 + 16, v + 16);
                         }
                     }
-                    const uint32_t al2 = cvt_f16x2(al, al);
+                    // P in two steps, as f16 has no factor below 2^-24
+                    const float al_a = fmaxf(al, 0x1p-14f), al_b = fminf(al * 0x1p14f, 1.0f);
+                    const uint32_t a2 = cvt_f16x2(al_a, al_a), b2 = cvt_f16x2(al_b, al_b);
 #pragma unroll 1
                     for (int c2 = chunk0; c2 < c; ++c2) {  // what the tile's P holds already
                         uint32_t p[16];
                         tmem_ld_32x32b_x16(s_at + 16 * c2, p);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) p[k] = hmul2(p[k], al2);
+                        for (int k = 0; k < 16; ++k) p[k] = hmul2(hmul2(p[k], a2), b2);
                         tmem_st_x16(s_at + 16 * c2, p);
                     }
                     tmem_st_wait();

@@ -117,3 +117,19 @@ def test_a_maximum_that_rises_inside_a_tile(orc, fmt, D, q, up):
     for causal in (True, False):
         out, lse = p.run(scale=LN2, causal=causal, out_dtype=torch.float32)
         kh.check_attention(out, lse, p.ref(scale=LN2, causal=causal), "%s D%d q%d" % (fmt, D, q))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_probabilities_are_rounded_once(orc, fmt, D):
+    """A probability is rounded when it is written, by at most half a step of f16, 2^-11 of it (all stay in f16's normal
+    range here); raising the base afterwards is a power of two.  So each step's weight is off by 2^-11, by 2 d (scores, see
+    check_attention), and by 2^-17 for fp32 sums of 128 terms and the quotient."""
+    p = _levels(fmt, D, 150, [-8, -3, 5, 9], seed=7)
+    p.lens[0] = 128  # one tile
+    out, lse = p.run(scale=LN2, causal=False, out_dtype=torch.float32)
+    r, l, absv, mass, _ = p.ref(scale=LN2, causal=False)
+    d = (2.0 ** -20 + 2.0 ** -22) * mass + 2.0 ** -22 * np.abs(l)
+    tol = (2 * d[..., None] + 2.0 ** -11 + 2.0 ** -17) * absv
+    err = np.abs(out.double().cpu().numpy() - r)
+    assert (err <= tol).all(), "off by %g of its tolerance" % np.nanmax(err / np.maximum(tol, 1e-300))
