@@ -4,7 +4,9 @@
 // of cached tokens into matrix-instruction operands in registers and keeps its own running softmax:
 //   S^T = K Q^T      m16n8k16, f16 x f16 -> fp32: tokens on M, rows on N, so that a group of up to
 //                    eight rows wastes nothing and a decoded K operand serves all rows;
-//   P   = 2^(s - m)  fp32; m is the warp's running maximum (log2 domain), raised only when a tile exceeds it;
+//   P   = 2^(c (s - m))  fp32, c > 0; m is the warp's running maximum of s, raised only when a tile exceeds it.  (The difference
+//                    is taken before the factor: tokens of one score then weigh the same however large it is, and no
+//                    exponent passes that of the maximum.)
 //   O^T = V^T P^T    head channels on M, tokens on K.
 // E2M1 codes convert to f16 exactly.  K: NVFP4 codes times their E4M3 scale are exact in f16 (six
 // significant bits, at most 2688); MXFP4's power-of-two scale multiplies the fp32 product of its
@@ -79,7 +81,7 @@ template <int FMT, int D, int NT>
 struct Warp {
     using C = Cfg<FMT, D, NT>;
     float o[NT][C::KS][4];
-    float base[NT][2], l[NT][2];  // probabilities are 2^(s - base): base is the running maximum - SHIFT
+    float base[NT][2], l[NT][2];  // probabilities are 2^(cs (s - base) + SHIFT): base is the running maximum of s
     int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];  // MXFP4: E8M0 code that stands for 2^9 in the factors, per 32 channels
 };
 
@@ -212,14 +214,16 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
     float s[C::TU][NT][4];
     scores<FMT, D, NT>(tile, qf, s);
 
-    // exponents s cs - base; one above SHIFT (all of them, before the first tile) raises the row's base
-    auto exponent = [&](int u, int n, int i, float base) {
-        float v = fmaf(s[u][n][i], cs[n][i & 1], -base);
+    // one above SHIFT (all of them, before the first tile) raises the row's base
+    auto masked = [&](int u, int n, int i, float v) {
         if constexpr (MASK) {
             const int pos = pos0 + 16 * u + 8 * (i >> 1) + g, r = 8 * n + 2 * t + (i & 1);
             if (pos < row_first[r] || pos >= row_end[r] || (skip >> u & 1u)) v = __int_as_float(0xff800000);
         }
         return v;
+    };
+    auto exponent = [&](int u, int n, int i, float base) {
+        return masked(u, n, i, fmaf(s[u][n][i] - base, cs[n][i & 1], C::SHIFT));
     };
     float x[C::TU][NT][4];
     float top = kNegMax;
@@ -240,11 +244,11 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
             for (int c = 0; c < 2; ++c) {
                 float m = kNegMax;
 #pragma unroll
-                for (int u = 0; u < C::TU; ++u) m = fmaxf(m, fmaxf(exponent(u, n, c, 0.0f), exponent(u, n, 2 + c, 0.0f)));
+                for (int u = 0; u < C::TU; ++u) m = fmaxf(m, fmaxf(masked(u, n, c, s[u][n][c]), masked(u, n, 2 + c, s[u][n][2 + c])));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float base = fmaxf(w.base[n][c], m - C::SHIFT);
-                al[c] = ex2(w.base[n][c] - base);
+                const float base = fmaxf(w.base[n][c], m);
+                al[c] = ex2((w.base[n][c] - base) * cs[n][c]);
                 w.base[n][c] = base;
                 w.l[n][c] *= al[c];
 #pragma unroll
@@ -412,6 +416,8 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
     Seq s = plan.s;
     float qscale = a.scale * 1.4426950408889634f;
     if constexpr (FMT == MXQ_NVFP4) qscale *= *a.g_k;
+    const uint32_t flip = qscale < 0.0f ? 0x80008000u : 0u;  // Q takes the sign
+    qscale = fabsf(qscale);
     uint32_t tiles = 0, nseg = 0;
 
 #pragma unroll 1
@@ -582,7 +588,7 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
                     uint32_t h[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = cvt_f16x2(__uint_as_float(y[k] << 16) * mul, __uint_as_float(y[k] & 0xFFFF0000u) * mul);
+                        h[k] = cvt_f16x2(__uint_as_float(y[k] << 16) * mul, __uint_as_float(y[k] & 0xFFFF0000u) * mul) ^ flip;
                     *reinterpret_cast<uint4*>(dst + i * 512) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 if (t == 0) {
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
 
-        // join the warps: each leaves (base, l, O); the sums are taken by all together
+        // join the warps: each leaves (base in units of log 2, l, O); the sums are taken by all together
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -687,7 +693,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
                 float x = w.l[i][c];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (g == 0) ml[warp * C::ROWS + 8 * i + 2 * t + c] = make_float2(w.base[i][c], x);
+                // (x is 0 where the warp has seen no token, and at least 2^SHIFT else)
+                if (g == 0)
+                    ml[warp * C::ROWS + 8 * i + 2 * t + c] = make_float2(x == 0.0f ? kNegMax : w.base[i][c] * cs[i][c] - C::SHIFT, x);
             }
 #pragma unroll
             for (int j = 0; j < C::KS; ++j) {

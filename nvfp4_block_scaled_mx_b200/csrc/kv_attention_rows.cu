@@ -654,14 +654,14 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     return fmaxf(m0, m1);
                 };
                 const float m = exponents(base);
-                if (__any_sync(0xffffffffu, m > kLimit)) {
+                if (__any_sync(0xffffffffu, m > kLimit || far_base(base))) {
                     // the product before the last of this group's tiles is done (its S was issued behind it); the tile's
                     // earlier P, which is read back below, is on its way: stores and loads of TMEM are not ordered
                     tmem_st_wait();
                     const float raw = exponents(0.0f);
                     // Bases are whole numbers, so that what is written already changes by a power of two, exactly, in
                     // l, O and P alike.  (A base at its start is far below; one that is no number makes the row none.)
-                    const float to = m > kLimit ? fmaxf(base, ceilf(raw - kStart)) : base, by = to - base;
+                    const float to = raw - base > kLimit ? fmaxf(base, ceilf(raw - kStart)) : base, by = to - base;
                     const float al = by < 126.0f ? __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(by)) << 23) : 0.0f;
                     base = to;
                     l *= al;
@@ -689,7 +689,10 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                         tmem_st_x16(s_at + 16 * c2, p);
                     }
                     tmem_st_wait();
-                    exponents(base);
+                    const float off = far_base(base) ? base : 0.0f;
+                    exponents(base - off);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(at_most(__uint_as_float(v[k]) - off, kLimit));
                 }
                 uint32_t p[16];
                 float l0 = 0.0f, l1 = 0.0f;

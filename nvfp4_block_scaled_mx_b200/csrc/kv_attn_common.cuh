@@ -281,6 +281,20 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// Large scores on tcgen05.  An exponent is fma(s, c, -base), and the base a row's rounded maximum less a few units.  From
+// |base| = 2^22 on, a step of fp32 is half a unit and more: what the product is rounded by then parts tokens of one score
+// from their own maximum, and what the base is rounded by lets exponents pass what P's f16 takes.  Such rows take
+// the branch that raises bases for every tile, where their exponents are rounded products less the base.  There exponents are
+// held at the limit, too: all tokens of one score weigh the same, whatever its size.
+__device__ __forceinline__ bool far_base(float base) {  // (a row that has seen no token is none)
+    return (__float_as_uint(base) & 0x7FFFFFFFu) - 0x4A800000u < 0x7F7FFFFFu - 0x4A800000u;
+}
+__device__ __forceinline__ float at_most(float x, float top) {  // (NaN stays)
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(top));
+    return r;
+}
+
 // N bytes (4, 8 or 16) of shared memory as words.
 template <int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N / 4]) {

@@ -133,3 +133,31 @@ def test_probabilities_are_rounded_once(orc, fmt, D):
     tol = (2 * d[..., None] + 2.0 ** -11 + 2.0 ** -17) * absv
     err = np.abs(out.double().cpu().numpy() - r)
     assert (err <= tol).all(), "off by %g of its tolerance" % np.nanmax(err / np.maximum(tol, 1e-300))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,q", [(64, 1, 3), (128, 5, 1), (256, 2, 2), (256, 5, 4), (128, 1, 20), (64, 1, 60), (128, 1, 150)])
+def test_large_scores(orc, fmt, D, G, q):
+    """Scores of 10^6 to 10^30, finite, and equal for every third token: those share the weight evenly, so the result is
+    known to the rounding of the probabilities however coarse fp32 is at such scores.  The log-sum-exp has fewer than 16
+    roundings of half a step of 2^-23, or as much where an exponent is held at the largest that f16 takes: 2^-20."""
+    n = 300
+    p = Problem(fmt, D, 1, G, 16, [n], [q], seed=5)
+    k = torch.zeros((n, 1, D), dtype=torch.bfloat16)
+    k[:, 0, 3] = -4.0
+    k[::3, 0, 3] = 4.0
+    v = _rand((n, 1, D), 6)
+    if fmt == "nvfp4":
+        p.gk, p.gv = np.float32(4 * 1.01 / 2688), np.float32(float(v.float().abs().max()) * 1.01 / 2688)
+        p.dk, p.dv = torch.tensor([p.gk], device="cuda"), torch.tensor([p.gv], device="cuda")
+    _rewrite(p, k, v)
+    p.q.zero_()
+    for x in (2e5, 3e6, 5.1e6, 7.7e6, 2.3e7, 9e8, 2e9, 1e12, 3e29):
+        p.q[..., 3] = x * (1 + torch.arange(p.q.shape[0] * G).reshape(-1, G) / 997.0)
+        out, lse = p.run(scale=1.0, causal=False, out_dtype=torch.float32)
+        r, l, absv, mass, floor = p.ref(scale=1.0, causal=False)
+        z = lse.double().cpu().numpy()
+        assert (np.abs(z - l) <= 2.0 ** -20 * np.abs(l)).all(), x
+        tol = 2.0 ** -24 * np.abs(r) + (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -16) * absv + 2.0 ** -28 * floor
+        err = np.abs(out.double().cpu().numpy() - r)
+        assert (err <= tol).all(), "%g: off by %g of its tolerance" % (x, np.nanmax(err / np.maximum(tol, 1e-300)))
