@@ -13,8 +13,9 @@
 // 32-element block.  Q is bf16 times a power of two per row (largest element in [2^7, 2^8)), exact in
 // f16 but for elements 2^-24 below the row's largest.  V: the scale multiplies P instead of the codes,
 // in f16: P is rounded to 11 bits (a bf16 P, 8 bits, would add as much error as the bf16 output has),
-// times 2^7 (NVFP4) or 2^4 (MXFP4) so that small probabilities keep their bits.  MXFP4 scales are taken
-// relative to the largest one met so far in the same 32 channels; blocks 2^23 below it vanish.
+// times 2^7 (NVFP4) or 2^4 (MXFP4) so that small probabilities keep their bits.  MXFP4 scales are taken relative to a
+// reference per 32 channels, the largest one met so far; a tile with scales that f16 does not hold beside it goes
+// another way (wide_step), band by band of 16 codes, so that no value is lost beside another, seen or not.
 // Sums, maxima and accumulators are fp32.
 //
 // Work is the list of all (sequence, row tile, kv head, token tile), cut evenly over the CTAs by every
@@ -82,8 +83,16 @@ struct Warp {
     using C = Cfg<FMT, D, NT>;
     float o[NT][C::KS][4];
     float base[NT][2], l[NT][2];  // probabilities are 2^(cs (s - base) + SHIFT): base is the running maximum of s
-    int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];  // MXFP4: E8M0 code that stands for 2^9 in the factors, per 32 channels
+    // MXFP4, per 32 channels: E8M0 code that stands for 2^9 in the factors and in O, the largest met within kRefMin and
+    // kRefMax.  (O is fp32 in units of 2^(ref - 136): it must not overflow beside values of 2^127, nor vanish beside
+    // a reference that follows them up; so values of 2^-90 keep their bits beside any.)
+    int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];
+    uint32_t bias;  // 13 - ref of the two blocks whose scales the lane checks, one a half
 };
+constexpr int kRefMin = 127 - 40, kRefMax = 127 + 40;
+// Scales that go into one product: codes ref - 13 to ref + 2, so factors 2^-4 to 2^11; with P of 2^4 at most the
+// product keeps f16's bits down to P = 2^-10, and holds the largest.
+constexpr int kBand = 16;
 
 template <int FMT, int D, int NT>
 __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
@@ -100,6 +109,7 @@ __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
     if constexpr (FMT == MXQ_MXFP4) {
 #pragma unroll
         for (int b = 0; b < C::U::NB; ++b) w.ref[b] = -1000;
+        w.bias = 1013u * 0x10001u;
     }
 }
 
@@ -202,15 +212,127 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
     }
 }
 
+// MXFP4, the V scales of a tile: a lane looks at four bytes, of a pair of tokens and two blocks (ten instructions a tile).
+template <int D, int NT>
+struct Scales {
+    using C = Cfg<MXQ_MXFP4, D, NT>;
+    using U = typename C::U;
+    static constexpr int WORDS = C::TU * 4 * U::NB, PER = U::NB / 2;  // of the tile, of a pair of tokens
+    static_assert(WORDS <= 32, "a word a lane");
+    uint32_t x[1];
+
+    __device__ __forceinline__ int word() const { return (threadIdx.x & 31) % WORDS; }
+    __device__ __forceinline__ int which() const { return word() % PER; }  // blocks 2 which, 2 which + 1
+    __device__ __forceinline__ void load(uint32_t tile) {
+        lds<4>(tile + word() / (4 * U::NB) * U::BYTES + U::OFF_VS + 4 * (word() % (4 * U::NB)), x);
+    }
+    __device__ __forceinline__ void mask(int pos0, int seen0, int seen1, uint32_t skip) {  // what no row sees counts as zeros
+        const int u = word() / (4 * U::NB);
+        x[0] &= skip >> u & 1u ? 0u : pair_mask(pos0 + 16 * u + word() % (4 * U::NB) / PER * 2, seen0, seen1);
+    }
+    // either token's codes, a block a half, and code - ref + 13, in [0, 16) if all is well (negative: a large unsigned one)
+    __device__ __forceinline__ uint32_t codes(int token) const { return prmt(x[0], 0u, token ? 0x4341u : 0x4240u); }
+    __device__ __forceinline__ uint32_t place(int token, const Warp<MXQ_MXFP4, D, NT>& w) const {
+        return __viaddmax_s16x2(codes(token), w.bias, 0x80008000u);
+    }
+    __device__ __forceinline__ bool odd(const Warp<MXQ_MXFP4, D, NT>& w) const { return ((place(0, w) | place(1, w)) & 0xFFF0FFF0u) != 0; }
+
+    // Moves the references (and O) up to the tile's scales where those pass them; whether scales remain that do not go
+    // into one product.
+    __device__ __forceinline__ bool refer(Warp<MXQ_MXFP4, D, NT>& w) const {
+        uint32_t most = __vmaxu2(codes(0), codes(1));
+#pragma unroll
+        for (int o = PER; o < 32; o <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
+#pragma unroll
+        for (int b = 0; b < U::NB; ++b) {
+            const int code = __shfl_sync(0xffffffffu, most, b >> 1) >> (16 * (b & 1)) & 0xFFFF, to = min(max(code, kRefMin), kRefMax);
+            if (code > w.ref[b] + 2 && to > w.ref[b]) {
+                const float f = scale_pow2(1.0f, max(w.ref[b] - to, -252));
+                w.ref[b] = to;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 2 * b; j < 2 * b + 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w.o[n][j][i] *= f;
+            }
+            const uint32_t half = static_cast<uint32_t>(13 - w.ref[b]) & 0xFFFFu;
+            if (which() == b >> 1) w.bias = b & 1 ? (w.bias & 0xFFFFu) | half << 16 : half;
+        }
+        // (code 0 counts as 0: the quantizer writes it for zeros, and for what is below 2^-124)
+        uint32_t out = 0;
+#pragma unroll
+        for (int token = 0; token < 2; ++token) out |= codes(token) & ~__vcmpltu2(place(token, w), kBand * 0x10001u);
+        return __any_sync(0xffffffffu, out != 0);
+    }
+};
+
+// O += V^T P^T of one unit in bands of 16 codes: each product from zero, added to O in fp32 times the band's power of two.
+template <int D, int NT>
+__device__ __forceinline__ void wide_values(Warp<MXQ_MXFP4, D, NT>& w, const uint32_t (&p)[NT][2], const uint32_t (&sb)[2][D / 64],
+                                            uint32_t unit) {
+    using U = KvUnit<MXQ_MXFP4, D>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int band = (kRefMin + 2 - 255) / kBand - 1; band <= (kRefMax + 1) / kBand; ++band) {
+        uint32_t fac[2][U::NB];
+        bool some = false;
+#pragma unroll
+        for (int b = 0; b < U::NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                fac[h][b] = 0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int code = sb[h][b >> 1] >> (16 * (b & 1) + 8 * half) & 0xFF, d = w.ref[b] + 2 - code - kBand * band;
+                    if (code == 0 || d < 0 || d >= kBand) continue;
+                    some = true;
+                    fac[h][b] |= static_cast<uint32_t>(26 - d) << (10 + 16 * half);
+                }
+            }
+        if (!__any_sync(0xffffffffu, some)) continue;
+        static_assert(kBand % 2 == 0, "half of it as a factor, twice");
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - kBand / 2 * band) << 23);
+#pragma unroll
+        for (int wd = 0; wd < D / 64; ++wd) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // bytes 4 wd .. 4 wd + 3 of both tokens' D / 16 in this lane's record
+                const int at0 = 4 * wd, at1 = D / 16 + 4 * wd;
+                const uint32_t at = unit + U::OFF_V + h * (4 * D) + lane * U::W;
+                uint32_t x[1], y[1];
+                lds<4>(at + at0 / U::W * (32 * U::W) + at0 % U::W, x);
+                lds<4>(at + at1 / U::W * (32 * U::W) + at1 % U::W, y);
+                e2m1x8((x[0] & 0x0F0F0F0Fu) | (y[0] << 4 & 0xF0F0F0F0u), a[2 * h]);
+                e2m1x8((x[0] >> 4 & 0x0F0F0F0Fu) | (y[0] & 0xF0F0F0F0u), a[2 * h + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int j = 4 * wd + i;
+                    float c[4];
+                    mma_f16_first(c, a[0][i], a[1][i], a[2][i], a[3][i], hmul2(p[n][0], fac[0][j / 2]), hmul2(p[n][1], fac[1][j / 2]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w.o[n][j][k] = fmaf(c[k] * f, f, w.o[n][j][k]);
+                }
+        }
+    }
+}
+
 // One token tile: scores, softmax update, O update.  pos0 is the tile's first token; MASK: some row does
-// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees; skip: units that no row sees.  (One copy of the code
+// not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees; skip: units that no row sees.  False for a
+// tile of MXFP4 with V scales far apart, which has to be taken again with WIDE.  (One copy of the code
 // with branches in it took 75 us where the two take 65: the branches part what the scheduler interleaves.)
-template <int FMT, int D, int NT, bool MASK>
-__device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, uint32_t qf, const float (&cs)[NT][2],
+template <int FMT, int D, int NT, bool MASK, bool WIDE = false>
+__device__ __forceinline__ bool tile_step(Warp<FMT, D, NT>& w, uint32_t tile, uint32_t qf, const float (&cs)[NT][2],
                                           const int* row_first, const int* row_end, int pos0, int seen0, int seen1, uint32_t skip) {
     using C = Cfg<FMT, D, NT>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr bool CHECK = FMT == MXQ_MXFP4 && !WIDE;
+    Scales<D, NT> scales;
+    if constexpr (CHECK) scales.load(tile);
     float s[C::TU][NT][4];
     scores<FMT, D, NT>(tile, qf, s);
 
@@ -236,7 +358,14 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
                 x[u][n][i] = exponent(u, n, i, w.base[n][i & 1]);
                 top = fmaxf(top, x[u][n][i]);
             }
-    if (__any_sync(0xffffffffu, top > C::SHIFT)) {
+    bool odd = false;
+    if constexpr (CHECK) {
+        if constexpr (MASK) scales.mask(pos0, seen0, seen1, skip);
+        odd = scales.odd(w);
+    }
+    if (__any_sync(0xffffffffu, top > C::SHIFT || odd)) {
+        if constexpr (CHECK)
+            if (__any_sync(0xffffffffu, odd) && scales.refer(w)) return false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float al[2];
@@ -312,49 +441,26 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
                 }
             }
         }
+        if constexpr (WIDE) {
+            wide_values<D, NT>(w, p, sb, unit);
+            continue;
+        }
         if constexpr (FMT == MXQ_NVFP4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int b = 0; b < U::NB; ++b) fac[h][b] = e4m3x2_f16x2(b & 1 ? sb[h][b >> 1] >> 16 : sb[h][b >> 1] & 0xFFFFu);
         } else {
-            // 2^(code - ref + 9): the exponent fields code - ref + 24 of both halves, 0 where that is below 1
-            auto codes = [&](int h, int b) {  // one a half
-                return prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);
-            };
-            auto fields = [&]() {
-                uint32_t most = 0;
+            // 2^(code - ref + 9): the exponent fields code - ref + 24 of both halves; 0 for code 0, as any ref is above 24
 #pragma unroll
-                for (int b = 0; b < U::NB; ++b) {
-                    const uint32_t bias = static_cast<uint32_t>((24 - w.ref[b]) & 0xFFFF) * 0x10001u;
+            for (int b = 0; b < U::NB; ++b) {
+                const uint32_t bias = static_cast<uint32_t>((24 - w.ref[b]) & 0xFFFF) * 0x10001u;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) fac[h][b] = __viaddmax_s16x2_relu(codes(h, b), bias, 0u);
-                    most = __vimax3_u16x2(most, fac[0][b], fac[1][b]);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t codes = prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);  // one a half
+                    fac[h][b] = __viaddmax_s16x2_relu(codes, bias, 0u) << 10;
                 }
-                return max(most & 0xFFFFu, most >> 16);
-            };
-            if (__any_sync(0xffffffffu, fields() > 26u)) {  // a code more than 2 above ref moves ref (and O) up
-#pragma unroll
-                for (int b = 0; b < U::NB; ++b) {
-                    const uint32_t hi = __vmaxu2(codes(0, b), codes(1, b));
-                    int code = static_cast<int>(max(hi & 0xFFFFu, hi >> 16));
-                    code = max(code, __shfl_xor_sync(0xffffffffu, code, 1));
-                    code = max(code, __shfl_xor_sync(0xffffffffu, code, 2));
-                    if (code > w.ref[b] + 2) {
-                        const float f = scale_pow2(1.0f, max(w.ref[b] - code, -252));
-                        w.ref[b] = code;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 2 * b; j < 2 * b + 2; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) w.o[n][j][i] *= f;
-                    }
-                }
-                fields();
             }
-#pragma unroll
-            for (int b = 0; b < U::NB; ++b) fac[0][b] <<= 10, fac[1][b] <<= 10;
         }
         // V codes: this lane's D / 16 bytes of both tokens of either pair
         uint32_t v[2][2][D / 64];
@@ -392,6 +498,32 @@ __device__ __forceinline__ void tile_step(Warp<FMT, D, NT>& w, uint32_t tile, ui
             }
         }
     }
+    return true;
+}
+
+// The same for token tile i of a segment of MXFP4, with scales far apart.  Rare, and out of line.
+template <int D, int NT>
+__device__ __noinline__ void wide_copy(Warp<MXQ_MXFP4, D, NT>& w, const uint8_t* smem, uint32_t buf, int i) {
+    using C = Cfg<MXQ_MXFP4, D, NT>;
+    const Segment& seg = *reinterpret_cast<const Segment*>(smem + C::OFF_SEG + buf * 64);
+    const float* row_scale = reinterpret_cast<const float*>(smem + C::OFF_ROW + buf * C::ROWS * 12);
+    const int* row_first = reinterpret_cast<const int*>(row_scale + C::ROWS);
+    const uint32_t slot = (seg.base + i) % C::STAGES;
+    float cs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) cs[n][c] = row_scale[8 * n + 2 * (threadIdx.x & 3) + c];
+    tile_step<MXQ_MXFP4, D, NT, true, true>(w, smem_u32(smem + C::OFF_RING + slot * C::TILE_BYTES),
+                                            smem_u32(smem + C::OFF_Q + buf * C::Q_BYTES), cs, row_first, row_first + C::ROWS,
+                                            seg.pos0 + i * C::TILE, seg.seen0, seg.seen1,
+                                            reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[slot]);
+}
+template <int D, int NT>
+__device__ __forceinline__ void wide_step(Warp<MXQ_MXFP4, D, NT>& w, const uint8_t* smem, uint32_t buf, int i) {
+    Warp<MXQ_MXFP4, D, NT> copy = w;  // (so that the state itself stays in registers)
+    wide_copy<D, NT>(copy, smem, buf, i);
+    w = copy;
 }
 
 // ------------------------------------------------------------------------------------- kernel
@@ -668,21 +800,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
         int first = warp - static_cast<int>(base % kWarps);
         if (first < 0) first += kWarps;
         int pos0 = seg.pos0 + first * C::TILE;
+        int i = first;
 #pragma unroll 1
-        for (int i = first; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
-            const uint32_t slot = (base + i) % C::STAGES;
-            if (!wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
-                dead = true;
-                break;
+        for (;;) {
+            bool done = true;
+#pragma unroll 1
+            for (; i < count; i += kWarps, pos0 += kWarps * C::TILE) {
+                const uint32_t slot = (base + i) % C::STAGES;
+                if (!wait_warp(&full[slot], (base + i) / C::STAGES & 1u, a.status, 0x40)) {
+                    dead = true;
+                    break;
+                }
+                const uint32_t tile = smem_u32(smem + C::OFF_RING + slot * C::TILE_BYTES);
+                const uint32_t skip = reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[slot];
+                done = skip == 0 && pos0 >= all0 && pos0 + C::TILE <= all1
+                           ? tile_step<FMT, D, NT, false>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, 0)
+                           : tile_step<FMT, D, NT, true>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, skip);
+                if (!done) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
             }
-            const uint32_t tile = smem_u32(smem + C::OFF_RING + slot * C::TILE_BYTES);
-            const uint32_t skip = reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[slot];
-            if (skip == 0 && pos0 >= all0 && pos0 + C::TILE <= all1)
-                tile_step<FMT, D, NT, false>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, 0);
-            else
-                tile_step<FMT, D, NT, true>(w, tile, qf, cs, row_first, row_end, pos0, seen0, seen1, skip);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (FMT == MXQ_NVFP4 || done) break;
+            if constexpr (FMT == MXQ_MXFP4) {
+                // (All that this needs is found again from the note: what the loop above kept for it in registers, it paid
+                // for in spills, 3 % of its time.)
+                int k = i;
+                asm volatile("" : "+r"(k));
+                wide_step<D, NT>(w, smem, buf, k);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[(seg.base + k) % C::STAGES]);
+                i = k + kWarps, pos0 = seg.pos0 + i * C::TILE;
+            }
         }
 
         // join the warps: each leaves (base in units of log 2, l, O); the sums are taken by all together

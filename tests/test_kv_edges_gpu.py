@@ -161,3 +161,36 @@ def test_large_scores(orc, fmt, D, G, q):
         tol = 2.0 ** -24 * np.abs(r) + (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -16) * absv + 2.0 ** -28 * floor
         err = np.abs(out.double().cpu().numpy() - r)
         assert (err <= tol).all(), "%g: off by %g of its tolerance" % (x, np.nanmax(err / np.maximum(tol, 1e-300)))
+
+
+@pytest.mark.parametrize("D,G,q", [s for s in SHAPES if s[0] == 256 or s[1] * s[2] <= 48])
+@pytest.mark.parametrize("big,small", [(24, 0), (60, 0), (90, 0), (0, -60), (60, -40)])
+def test_mxfp4_values_of_any_scale(orc, D, G, q, big, small):
+    """Values of 2^small beside ones of 2^big: tokens that a row does not see, and ones whose probability is 0, leave the
+    others' values as they are.  In every second block of 32 channels the large values are elsewhere."""
+    n = 150
+    p = Problem("mxfp4", D, 1, G, 16, [n, 40], [q, 1], seed=D + q)
+    f = np.full((n, D), 2.0 ** small)
+    block = np.arange(D) // 32 % 2
+    loud = [n - 1, n - max(q // 2, 1), 7, 100]  # seen by the last rows alone, and by all
+    for t in loud:
+        f[t, block == (t == 100)] = 2.0 ** big
+    k = _rand((n, 1, D), 1)
+    for t in (7, 100):
+        k[t, 0, 3] = -2.0 ** 16  # so that its probability is 0
+    p.q[..., 3] = 4.0
+    v = (_rand((n, 1, D), 2).double() * torch.from_numpy(f)[:, None]).to(torch.bfloat16)
+    _rewrite(p, k, v)
+    out, lse = p.run(out_dtype=torch.float32)
+    kh.check_attention(out, lse, _reference(p, {0: [7, 100]}), "2^%d beside 2^%d" % (big, small))
+
+
+@pytest.mark.parametrize("D,G,q", [(64, 1, 3), (128, 5, 4), (256, 2, 3)])
+def test_mxfp4_values_that_are_no_numbers_stay_with_the_rows_that_see_them(orc, D, G, q):
+    p = Problem("mxfp4", D, 1, G, 16, [90], [q], seed=12)
+    pos = kh.positions(D, "mxfp4")
+    ref = p.ref()
+    t = 89  # seen by the last row alone
+    p.cache[p.table[0, t // 16], :, 0, pos[3][t % 16]] = 0xFF
+    out, lse = p.run(out_dtype=torch.float32)
+    kh.check_attention(out[:-1], lse[:-1], tuple(x[:-1] for x in ref), "0xFF")
