@@ -304,11 +304,11 @@ size_t mxq_kv_attention_workspace_size(int64_t batch, int64_t max_q, int heads, 
  *                logarithm of the softmax's denominator, or NULL.  A row that sees no token gets zeros and
  *                -inf.  Rows of no sequence are left as they were.
  *   workspace    (device) at least mxq_kv_attention_workspace_size(...) bytes; needs no preparation.
- * max_pages * page_size <= 2^30 - 1024.  fp32 softmax and sums; probabilities are rounded to f16 (11 bits)
- * for the product with V.  MXFP4 blocks of V whose scale is 2^23 or more below the largest in the same 32
- * channels (over the tokens that are taken together, at most all of the sequence's) count as zero.  Scale
- * bytes that are not numbers, which the quantizer never writes, have no effect where no row sees the token;
- * rows that see it, and in MXFP4 their neighbours of the same sequence, get anything.  Results do not
+ * max_pages * page_size <= 2^30 - 1024.  Scores, softmax and sums are fp32.  Rounded to fewer bits are q, to 2^-32 of its
+ * row's largest element (MXFP4 with many rows: not at all), and probabilities, for the product with V, to f16: 2^-11 of
+ * one, or 2^-28 of the row's largest where that is more; with few rows their product with V's scale once more so; MXFP4
+ * with many rows keeps 16 bits.  MXFP4 values below 2^-90 and blocks of scale byte 0 may count as zero.  Scale bytes that
+ * are not numbers, which the quantizer never writes, have an effect on rows that see the token alone.  Results do not
  * depend on timing.  Two launches.  Calls that may run at the same time need a workspace each.
  */
 int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_t q_head_stride, const void* cache,

@@ -4,12 +4,14 @@
 //
 // With many rows the tensor work counts, so it runs on tcgen05 (kind::f16, fp32 accumulators in TMEM), one
 // CTA per SM, tiles of 128 tokens:
-//   S = Q K^T   Q [128 rows x D] and K in shared memory, 128-byte swizzle; Q once per segment, f16 times a power
-//               of two per row; K as f16, codes times scale: E4M3 (exact), E8M0 relative to the token's largest
-//               (exact down to 2^-27 of it), which the softmax multiplies S by;
-//   P = 2^(s - base), f16, in TMEM; one thread has one row, so the softmax needs no shuffles;
-//   O += P V    V decoded as f16 into shared memory transposed ([channel][token]); E8M0 scales relative to a
-//               running reference per 32 channels (blocks 2^23 below it vanish), which O follows.
+//   S = Q K^T   Q [128 rows x D] and K in shared memory, 128-byte swizzle; Q once per segment, times a power of two per
+//               row; K codes times scale;
+//   P = 2^(s - base) in TMEM; one thread has one row, so the softmax needs no shuffles;
+//   O += P V    V codes times scale in shared memory, transposed ([channel][token]).
+// NVFP4 operands are f16, which holds codes times E4M3 scales exactly, and P rounded to 11 bits.  MXFP4 operands are bf16:
+// codes times E8M0 scales need two bits and the whole range of exponents, which f16 does not have.  (As f16 relative to a
+// running reference, blocks 2^23 below it vanished, and eight warps agreed on that reference in every tile: a chunk of 700
+// took 310 us.)  P is two bf16 then, its upper and its lower 8 bits, and O two products.
 // Roles: two groups of 4 softmax warps (their TMEM lanes are the rows) that take the tiles in turn, each with
 // its own S and O, so that one group's exponentials run beside the other's products; 4 warps that decode K
 // (32 tokens of a tile each) and 8 that decode V (16 tokens); one warp that feeds raw tiles by bulk copies;
@@ -66,29 +68,24 @@ struct RCfg {
     static constexpr int OFF_RAW = OFF_Q + Q16;
     static constexpr int OFF_ML = OFF_RAW + STAGES * RAW;  // [2 groups][128 lanes] (base, l)
     static constexpr int OFF_QS = OFF_ML + 2 * 128 * 8;  // scale of each row's scores, two buffers
-    // MXFP4: of the last four tiles, each token's key factor, and the reference codes and largest codes of V's blocks
-    static constexpr int OFF_KF = OFF_QS + 2 * 128 * 4;
-    static constexpr int OFF_REF = OFF_KF + (FMT == MXQ_MXFP4 ? 4 * kTokens * 4 : 0);
-    static constexpr int OFF_MAX = OFF_REF + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
     // of the last eight tiles, a bit for each unit of a page outside the cache (a tile is eight behind only when its
     // softmax is done: it is decoded before the third tile behind it is fed, the second's V waits for its product)
-    static constexpr int OFF_SKIP = OFF_MAX + (FMT == MXQ_MXFP4 ? 4 * 4 * 4 : 0);
+    static constexpr int OFF_SKIP = OFF_QS + 2 * 128 * 4;
     static constexpr int OFF_SEG = OFF_SKIP + 8 * 4;
     static constexpr int OFF_BAR = OFF_SEG + 2 * 64;
-    static constexpr int NBARS = 2 * STAGES + 12 + 1 + 4;
+    static constexpr int NBARS = 2 * STAGES + 10 + 1 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int BYTES = OFF_TMEM + 16 + 1024;  // and the alignment
     static constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each: S 128 columns, O D columns
 };
 
 struct RowBars {
-    uint64_t *raw_full, *raw_empty, *kf, *vf, *sf, *pf, *od, *vm, *qf, *seg_full, *seg_empty;
+    uint64_t *raw_full, *raw_empty, *kf, *vf, *sf, *pf, *od, *qf, *seg_full, *seg_empty;
     __device__ __forceinline__ RowBars(uint8_t* at, int stages) {
         uint64_t* b = reinterpret_cast<uint64_t*>(at);
         raw_full = b, raw_empty = b + stages, b += 2 * stages;
         // of tile n, at n & 1: K and V decoded, S done (K may be overwritten), P written, O done (V, P may be)
-        // (MXFP4: vm, the largest codes of V's blocks are there)
-        kf = b, vf = b + 2, sf = b + 4, pf = b + 6, od = b + 8, vm = b + 10, b += 12;
+        kf = b, vf = b + 2, sf = b + 4, pf = b + 6, od = b + 8, b += 10;
         qf = b, b += 1;
         seg_full = b, seg_empty = b + 2;
     }
@@ -99,6 +96,42 @@ template <class C>
 __device__ __forceinline__ uint32_t skipped(const uint8_t* smem, uint32_t n) {
     return reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_SKIP)[n & 7];
 }
+
+// MXFP4 operands are codes times 2^(scale code - 127 - offset): scale codes up to 255 stay finite with what E2M1 adds, and
+// sums of products with P (2^15 at most) or Q (2^8) within fp32 for values up to 2^113 and more.
+constexpr int kKeyOffset = 12, kValueOffset = 20;
+
+// 8 E2M1 codes as 4 bf16x2, times 2^-126: byte i of w becomes o[i], its low nibble in the low half (see dequant8_mul).
+__device__ __forceinline__ void e2m1x8_tiny(uint32_t w, uint32_t (&o)[4]) {
+    const uint32_t ev = w & 0x0F0F0F0Fu, od = w >> 4 & 0x0F0F0F0Fu;
+    o[0] = prmt(ev, od, 0x8480u) * 0x1040u & 0x81C081C0u;
+    o[1] = prmt(ev, od, 0x9591u) * 0x1040u & 0x81C081C0u;
+    o[2] = prmt(ev, od, 0xA6A2u) * 0x1040u & 0x81C081C0u;
+    o[3] = prmt(ev, od, 0xB7B3u) * 0x1040u & 0x81C081C0u;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Scale codes c, one a half: bf16x2 factors for e2m1x8_tiny, 2^(126 + c - 127 - offset) as far as bf16 goes, and what is
+// left of codes behind that.
+template <int OFFSET>
+struct MxFactor {
+    static constexpr uint32_t LAST = 128 + OFFSET;  // 2^127
+    uint32_t first, rest;
+    bool more;
+    __device__ __forceinline__ explicit MxFactor(uint32_t c) {
+        const uint32_t low = __vminu2(c, LAST * 0x10001u);
+        first = (low + (126u - OFFSET) * 0x10001u) << 7;
+        rest = (c - low + 127u * 0x10001u) << 7;
+        more = c != low;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const {
+        x = bmul2(x, first);
+        return more ? bmul2(x, rest) : x;
+    }
+};
 
 // Feeds raw tiles (whole warp): eight lanes have a unit each; neighbouring units of a page go as one copy.
 template <int FMT, int D, bool QUAD>
@@ -222,9 +255,10 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
 template <int FMT, int D, bool QUAD>
 __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, uint32_t tmem) {
     using C = RCfg<FMT, D, QUAD>;
-    // kind::f16 with f16 operands (formats 0), fp32 accumulator
-    constexpr uint32_t IDESC_S = (1u << 4) | ((kTokens >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t IDESC_O = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+    // kind::f16 with f16 (formats 0) or bf16 operands (formats 1), fp32 accumulator
+    constexpr uint32_t KIND = (1u << 4) | (FMT == MXQ_MXFP4 ? 1u << 7 | 1u << 10 : 0u);
+    constexpr uint32_t IDESC_S = KIND | ((kTokens >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t IDESC_O = KIND | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
     const uint32_t q = smem_u32(smem + C::OFF_Q);
     auto product = [&](uint32_t t, bool first) -> bool {  // O += P V of tile t
         if (!wait_warp(&bar.vf[t & 1], t >> 1 & 1u, a.status, 0x53)) return false;
@@ -233,10 +267,13 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
         if (elect_one()) {
             const uint32_t v = smem_u32(smem + C::OFF_V + (t & 1) * C::V16);
 #pragma unroll
-            for (int j = 0; j < kTokens / 16; ++j)
-                mma_bf16_ts(tmem + C::O_COL + (t & 1) * D, tmem + C::S_COL + (t & 1) * 128 + j * 8,
-                            smem_desc(v + (j >> 2) * (D * 128) + (j & 3) * 32, 16, 1024, kLayoutSwizzle128B), IDESC_O,
-                            first && j == 0 ? 0u : 1u);
+            for (int j = 0; j < kTokens / 16; ++j) {
+                const uint64_t vd = smem_desc(v + (j >> 2) * (D * 128) + (j & 3) * 32, 16, 1024, kLayoutSwizzle128B);
+                const uint32_t o = tmem + C::O_COL + (t & 1) * D;
+                const uint32_t p = tmem + C::S_COL + (t & 1) * 128 + (FMT == MXQ_MXFP4 ? (j >> 1) * 32 + (j & 1) * 8 : j * 8);
+                mma_bf16_ts(o, p, vd, IDESC_O, first && j == 0 ? 0u : 1u);
+                if constexpr (FMT == MXQ_MXFP4) mma_bf16_ts(o, p + 16, vd, IDESC_O, 1u);  // P's lower bits
+            }
             tc_commit(&bar.od[t & 1]);
         }
         __syncwarp();
@@ -268,7 +305,7 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
                                  smem_desc(k + at, 16, 1024, kLayoutSwizzle128B), IDESC_S, j == 0 ? 0u : 1u);
                     }
                     tc_commit(&bar.sf[t & 1]);
-                    mbar_arrive(&bar.sf[t & 1]);  // hands on what the feeding and the key warps noted of the tile
+                    mbar_arrive(&bar.sf[t & 1]);  // hands on what the feeding warp noted of the tile
                 }
                 __syncwarp();
             }
@@ -279,7 +316,7 @@ __device__ __forceinline__ void rows_mma(const KvAttnArgs& a, uint8_t* smem, con
     }
 }
 
-// MXFP4 scale codes of a token's key blocks, one a byte (0 behind the last), and the largest of them.
+// MXFP4 scale codes of a token's key blocks, one a byte.
 template <int D>
 __device__ __forceinline__ uint32_t key_codes(uint32_t at) {
     if constexpr (D == 64) return ld_shared_u16(at);
@@ -287,16 +324,12 @@ __device__ __forceinline__ uint32_t key_codes(uint32_t at) {
     lds<4>(at, x);
     return x[0];
 }
-__device__ __forceinline__ uint32_t largest_code(uint32_t c) {
-    const uint32_t m = __vmaxu2(c & 0x00FF00FFu, c >> 8 & 0x00FF00FFu);
-    return max(m & 0xFFFFu, m >> 16);
-}
 
 // Keys of units u, u + 1: a lane has quarter q of token r: 32-bit words of 8 elements, 16 bytes each once
 // decoded.  Eight neighbouring lanes have four tokens and two quarters, whose chunks meet different banks.
 // `loaded` is called once the raw bytes are in registers; it waits for the operand's place.
 template <int FMT, int D, bool QUAD, class Loaded>
-__device__ __forceinline__ bool keys(uint32_t raw, uint32_t k16, int u, float* factors, Loaded loaded) {
+__device__ __forceinline__ bool keys(uint32_t raw, uint32_t k16, int u, Loaded loaded) {
     using U = typename RCfg<FMT, D, QUAD>::U;
     const int lane = threadIdx.x & 31;
     const int r0 = (lane >> 3 & 1) * 4 + (lane >> 1 & 3), q = (lane >> 4) * 2 + (lane & 1);
@@ -316,28 +349,26 @@ __device__ __forceinline__ bool keys(uint32_t raw, uint32_t k16, int u, float* f
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t row = u * 16 + 8 * i + r0;
-        uint32_t f = 0, most = 0;
-        if constexpr (FMT == MXQ_NVFP4)
-            f = e4m3x2_f16x2(sc[i]);
-        else
-            most = largest_code(sc[i]);
-        // S of the token is in units of 2^(most - 127 - 13)
-        if (FMT == MXQ_MXFP4 && q == 0) factors[row] = __uint_as_float(most > 13 ? (most - 13) << 23 : 0u);
+        uint32_t f = 0;
+        if constexpr (FMT == MXQ_NVFP4) f = e4m3x2_f16x2(sc[i]);
 #pragma unroll
         for (int k = 0; k < U::W / 4; ++k) {
-            uint32_t f2, chunk;  // factor of the word's 8 elements, twice; their place in the row
+            uint32_t o[4], chunk;  // of the word's 8 elements; their place in the row
             if constexpr (FMT == MXQ_NVFP4) {
-                f2 = k < 2 ? prmt(f, f, 0x1010u) : prmt(f, f, 0x3232u);
+                const uint32_t f2 = k < 2 ? prmt(f, f, 0x1010u) : prmt(f, f, 0x3232u);
                 chunk = q * (U::W / 4) + k;
-            } else {  // word k lies in block k: 2^(code - most + 13), exact down to 2^-27 below the token's largest
-                const int field = static_cast<int>(sc[i] >> (8 * k) & 0xFFu) - static_cast<int>(most) + 28;
-                f2 = static_cast<uint32_t>(max(field, 0)) * 0x04000400u;
+                e2m1x8(w[i][k], o);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] = hmul2(o[x], f2);
+            } else {  // word k lies in block k
+                const MxFactor<kKeyOffset> f2((sc[i] >> (8 * k) & 0xFFu) * 0x10001u);
                 chunk = 4 * k + q;
+                e2m1x8_tiny(w[i][k], o);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] = f2.of(o[x]);
             }
-            uint32_t o[4];
-            e2m1x8(w[i][k], o);
             st_shared_v4(k16 + (chunk >> 3) * (kTokens * 128) + row * 128 + (((chunk & 7) ^ (r0 & 7)) << 4),
-                         make_uint4(hmul2(o[0], f2), hmul2(o[1], f2), hmul2(o[2], f2), hmul2(o[3], f2)));
+                         make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
     return true;
@@ -346,7 +377,7 @@ __device__ __forceinline__ bool keys(uint32_t raw, uint32_t k16, int u, float* f
 // Values of unit u, transposed: a lane has tokens 8 h + 2 t, + 1 and channels 16 j + 2 g, + 1.
 template <int FMT, int D, bool QUAD, class Loaded>
 __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool edge, int pos0, int seen0, int seen1,
-                                       uint8_t* smem, const RowBars& bar, uint32_t n, int (&ref)[4], int* status, Loaded loaded) {
+                                       const uint8_t* smem, uint32_t n, Loaded loaded) {
     using C = RCfg<FMT, D, QUAD>;
     using U = typename C::U;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -362,8 +393,8 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
     }
     if (!loaded()) return false;
     if (edge) {
-        // tokens that no row sees: 0, whatever the bytes are; a NaN (the quantizer writes none): the
-        // largest number, as 0 times it has to be 0 for the rows that do not see the token
+        // tokens that no row sees: 0, whatever the bytes are; a NaN of E4M3 (the quantizer writes none): the largest
+        // number, as 0 times it has to be 0 for the rows that do not see the token (E8M0's stands for 2^128 here)
         const uint32_t skip = skipped<C>(smem, n);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -375,59 +406,36 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
             }
         }
     }
-    uint32_t fac[2][U::NB];  // f16x2 of the two tokens
-    if constexpr (FMT == MXQ_NVFP4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int b = 0; b < U::NB; ++b) fac[h][b] = e4m3x2_f16x2(b & 1 ? sb[h][b >> 1] >> 16 : sb[h][b >> 1] & 0xFFFFu);
-    } else {
-        // Factors 2^(code - ref + 9) with a reference per 32 channels that the whole tile shares: the largest
-        // code of the segment so far, moved up when one exceeds it by more than 2 (the softmax warps scale O
-        // then).  The eight warps agree on a tile's largest codes in shared memory.
-        int* most = reinterpret_cast<int*>(smem + C::OFF_MAX) + (n & 3) * 4;
-#pragma unroll
-        for (int b = 0; b < U::NB; ++b) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fac[h][b] = prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u);  // the codes, one a half
-            const uint32_t m = __vmaxu2(fac[0][b], fac[1][b]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-            if (lane == b) atomicMax(&most[b], static_cast<int>(top));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.vm[n & 1]);
-        if (!wait_warp(&bar.vm[n & 1], n >> 1 & 1u, status, 0x62)) return false;
-        // tile n + 2's, which nobody looks at before all have passed the next wait
-        if (u == 0 && lane < 4) reinterpret_cast<int*>(smem + C::OFF_MAX)[((n + 2) & 3) * 4 + lane] = 0;
-#pragma unroll
-        for (int b = 0; b < U::NB; ++b) {
-            const int top = most[b];
-            if (top > ref[b] + 2) ref[b] = top;
-            const uint32_t bias = static_cast<uint32_t>((24 - ref[b]) & 0xFFFF) * 0x10001u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fac[h][b] = __viaddmax_s16x2_relu(fac[h][b], bias, 0u) << 10;
-            if (u == 0 && lane == b) reinterpret_cast<int*>(smem + C::OFF_REF)[(n & 3) * 4 + b] = ref[b];
-        }
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t chunk = (u & 3) * 2 + h;  // of 8 tokens in the block of 64
         // lanes with g >= 4 take the odd channel first: else rows 2 g and 2 (g + 4) would meet the same banks
         const uint32_t even = to + ((chunk ^ (2 * g & 7)) << 4), odd = to + 128 + ((chunk ^ ((2 * g + 1) & 7)) << 4);
         const uint32_t at0 = g < 4 ? even : odd, at1 = g < 4 ? odd : even;
+        auto scaled = [&](uint32_t x, int j) {  // of the two tokens, channel 16 j + ...
+            const int b = FMT == MXQ_NVFP4 ? j : j / 2;
+            if constexpr (FMT == MXQ_NVFP4)
+                return hmul2(x, e4m3x2_f16x2(b & 1 ? sb[h][b >> 1] >> 16 : sb[h][b >> 1] & 0xFFFFu));
+            else
+                return MxFactor<kValueOffset>(prmt(sb[h][b >> 1], 0u, b & 1 ? 0x4342u : 0x4140u)).of(x);
+        };
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
             const uint32_t x = w[h][wd], y = w[h][D / 64 + wd];
             const uint32_t lo = (x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), hi = (x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
             uint32_t v0[4], v1[4];
-            e2m1x8(g < 4 ? lo : hi, v0);
-            e2m1x8(g < 4 ? hi : lo, v1);
+            if constexpr (FMT == MXQ_NVFP4) {
+                e2m1x8(g < 4 ? lo : hi, v0);
+                e2m1x8(g < 4 ? hi : lo, v1);
+            } else {
+                e2m1x8_tiny(g < 4 ? lo : hi, v0);
+                e2m1x8_tiny(g < 4 ? hi : lo, v1);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int j = 4 * wd + k;
-                const uint32_t f = fac[h][FMT == MXQ_NVFP4 ? j : j / 2];
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(hmul2(v0[k], f)) : "memory");
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(hmul2(v1[k], f)) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at0 + j * 2048), "r"(scaled(v0[k], j)) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at1 + j * 2048), "r"(scaled(v1[k], j)) : "memory");
             }
         }
     }
@@ -437,11 +445,14 @@ __device__ __forceinline__ bool values(uint32_t raw, uint32_t v16, int u, bool e
 template <int FMT>
 __device__ __forceinline__ float score_scale(const KvAttnArgs& a) {
     float s = a.scale * 1.4426950408889634f;
-    if constexpr (FMT == MXQ_NVFP4) s *= *a.g_k;
+    if constexpr (FMT == MXQ_NVFP4)
+        s *= *a.g_k;
+    else
+        s *= static_cast<float>(1 << kKeyOffset);
     return s;
 }
 
-// Q rows of a segment: f16 times a power of two (largest element in [2^7, 2^8)).  Of eight warps each takes every
+// Q rows of a segment, times a power of two (largest element in [2^7, 2^8)).  Of eight warps each takes every
 // eighth row, all its lanes one row at a time; QUAD: the row stands in all four groups of lanes.
 template <int FMT, int D, bool QUAD>
 __device__ __forceinline__ void queries(const KvAttnArgs& a, const Segment& note, uint8_t* smem, float* qs, float qscale, int warp) {
@@ -485,7 +496,11 @@ __device__ __forceinline__ void queries(const KvAttnArgs& a, const Segment& note
                                                             (((c & 7) ^ (tr & 7)) << 4) + e % 8 * 2);
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i)
-                    dst[i] = cvt_f16x2(__uint_as_float(x[k][i] << 16) * mul, __uint_as_float(x[k][i] & 0xFFFF0000u) * mul);
+                {
+                    const float q0 = __uint_as_float(x[k][i] << 16) * mul, q1 = __uint_as_float(x[k][i] & 0xFFFF0000u) * mul;
+                    // (bf16: exact, so its upper halves)
+                    dst[i] = FMT == MXQ_MXFP4 ? prmt(__float_as_uint(q0), __float_as_uint(q1), 0x7632u) : cvt_f16x2(q0, q1);
+                }
             }
         }
     }
@@ -493,7 +508,7 @@ __device__ __forceinline__ void queries(const KvAttnArgs& a, const Segment& note
     __syncwarp();
 }
 
-// Decodes tiles to f16 operands: warps 0-3 the keys of two units each, warps 4-11 the values of one.
+// Decodes tiles to 16-bit operands: warps 0-3 the keys of two units each, warps 4-11 the values of one.
 template <int FMT, int D, bool QUAD>
 __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, const RowBars& bar, int warp) {
     using C = RCfg<FMT, D, QUAD>;
@@ -519,7 +534,6 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
             queries<FMT, D, QUAD>(a, note, smem, reinterpret_cast<float*>(smem + C::OFF_QS) + buf * 128, qscale, warp - kKeyWarps);
             if (lane == 0) mbar_arrive(bar.qf);
         }
-        int ref[4] = {-1000, -1000, -1000, -1000};  // MXFP4: E8M0 codes that stand for 2^9 in V's factors
 #pragma unroll 1
         for (int i = 0; i < count; ++i, pos0 += kTokens) {
             const uint32_t n = base + i, slot = n % C::STAGES;
@@ -533,12 +547,10 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
                                         : wait_warp(&bar.od[n & 1], (n >> 1 & 1u) ^ 1u, a.status, 0x5c);
             };
             if (warp < kKeyWarps) {
-                if (!keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp,
-                                        reinterpret_cast<float*>(smem + C::OFF_KF) + (n & 3) * kTokens, loaded))
-                    return;
+                if (!keys<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_K + (n & 1) * C::K16), 2 * warp, loaded)) return;
             } else {
                 if (!values<FMT, D, QUAD>(raw, smem_u32(smem + C::OFF_V + (n & 1) * C::V16), warp - kKeyWarps,
-                                          skipped<C>(smem, n) != 0 || pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, bar, n, ref, a.status, loaded))
+                                          skipped<C>(smem, n) != 0 || pos0 < all0 || pos0 + kTokens > all1, pos0, seen0, seen1, smem, n, loaded))
                     return;
             }
             fence_proxy_async_smem();
@@ -548,10 +560,10 @@ __device__ __forceinline__ void rows_decode(const KvAttnArgs& a, uint8_t* smem, 
     }
 }
 
-// A value of O: for MXFP4 relative to its 32 channels' reference code, which stands for 2^9.
+// A value of O.
 template <int FMT>
-__device__ __forceinline__ float value(uint32_t x, int ref) {
-    return FMT == MXQ_MXFP4 ? scale_pow2(__uint_as_float(x), max(ref, 0) - 136) : __uint_as_float(x);
+__device__ __forceinline__ float value(uint32_t x) {
+    return FMT == MXQ_MXFP4 ? __uint_as_float(x) * static_cast<float>(1 << kValueOffset) : __uint_as_float(x);
 }
 
 // Softmax: a thread has one row (QUAD: one row and a quarter of each tile's tokens) in every second tile.
@@ -602,7 +614,6 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
         float base = kNegMax, l = 0.0f;
         const uint32_t o_at = lanes + C::O_COL + group * D;
         bool begun = false;  // O holds something
-        int oref[4] = {0, 0, 0, 0};  // MXFP4: the reference codes that O is relative to
         // tiles n with n & 1 = group
 #pragma unroll 1
         for (uint32_t n = note.base + ((note.base ^ group) & 1u); n < note.base + note.count; n += 2) {
@@ -611,7 +622,6 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                 break;
             }
             tc_fence_after();
-            const float* kfac = reinterpret_cast<const float*>(smem + C::OFF_KF) + (n & 3) * kTokens;
             const uint32_t s_at = lanes + C::S_COL + group * 128;
             const int pos0 = note.pos0 + static_cast<int>(n - note.base) * kTokens;
             const bool edge = skipped<C>(smem, n) != 0 || pos0 < note.all0 || pos0 + kTokens > note.all1;
@@ -621,16 +631,6 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     tmem_ld_32x32b_x32(s_at + 32 * c, v);
                     tmem_ld_wait();
                     float m0 = kNegMax, m1 = kNegMax;
-                    if constexpr (FMT == MXQ_MXFP4) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(kfac + 32 * c + k);
-                            v[k] = __float_as_uint(__uint_as_float(v[k]) * f.x);
-                            v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) * f.y);
-                            v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) * f.z);
-                            v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) * f.w);
-                        }
-                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), cs, -from));
                     if (edge) {
@@ -676,17 +676,30 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                             tmem_st_x16(o_at + k0 + 16, v + 16);
                         }
                     }
-                    // P in two steps, as f16 has no factor below 2^-24
-                    const float al_a = fmaxf(al, 0x1p-14f), al_b = fminf(al * 0x1p14f, 1.0f);
-                    const uint32_t a2 = cvt_f16x2(al_a, al_a), b2 = cvt_f16x2(al_b, al_b);
+                    if constexpr (FMT == MXQ_MXFP4) {
+                        const uint32_t a2 = prmt(__float_as_uint(al), 0u, 0x3232u);
 #pragma unroll 1
-                    for (int c2 = chunk0; c2 < c; ++c2) {  // what the tile's P holds already
-                        uint32_t p[16];
-                        tmem_ld_32x32b_x16(s_at + 16 * c2, p);
-                        tmem_ld_wait();
+                        for (int c2 = 0; c2 < c; ++c2) {  // what the tile's P holds already
+                            tmem_ld_32x32b_x32(s_at + 32 * c2, v);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) p[k] = hmul2(hmul2(p[k], a2), b2);
-                        tmem_st_x16(s_at + 16 * c2, p);
+                            for (int k = 0; k < 32; ++k) v[k] = bmul2(v[k], a2);
+                            tmem_st_x16(s_at + 32 * c2, v);
+                            tmem_st_x16(s_at + 32 * c2 + 16, v + 16);
+                        }
+                    } else {
+                        // in two steps, as f16 has no factor below 2^-24
+                        const float al_a = fmaxf(al, 0x1p-14f), al_b = fminf(al * 0x1p14f, 1.0f);
+                        const uint32_t a2 = cvt_f16x2(al_a, al_a), b2 = cvt_f16x2(al_b, al_b);
+#pragma unroll 1
+                        for (int c2 = chunk0; c2 < c; ++c2) {
+                            uint32_t p[16];
+                            tmem_ld_32x32b_x16(s_at + 16 * c2, p);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) p[k] = hmul2(hmul2(p[k], a2), b2);
+                            tmem_st_x16(s_at + 16 * c2, p);
+                        }
                     }
                     tmem_st_wait();
                     const float off = far_base(base) ? base : 0.0f;
@@ -694,17 +707,29 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(at_most(__uint_as_float(v[k]) - off, kLimit));
                 }
-                uint32_t p[16];
+                uint32_t p[FMT == MXQ_MXFP4 ? 32 : 16];
                 float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float e0 = ex2(__uint_as_float(v[2 * k])), e1 = ex2(__uint_as_float(v[2 * k + 1]));
                     l0 += e0;
                     l1 += e1;
-                    p[k] = cvt_f16x2(e0, e1);
+                    if constexpr (FMT == MXQ_MXFP4) {  // the upper 8 bits, cut off, and the next 8, rounded: 2^-16 of e at most is lost
+                        p[k] = prmt(__float_as_uint(e0), __float_as_uint(e1), 0x7632u);
+                        const __nv_bfloat162 rest = __floats2bfloat162_rn(e0 - __uint_as_float(__float_as_uint(e0) & 0xFFFF0000u),
+                                                                          e1 - __uint_as_float(__float_as_uint(e1) & 0xFFFF0000u));
+                        p[16 + k] = *reinterpret_cast<const uint32_t*>(&rest);
+                    } else {
+                        p[k] = cvt_f16x2(e0, e1);
+                    }
                 }
                 l += l0 + l1;
-                tmem_st_x16(s_at + 16 * c, p);
+                if constexpr (FMT == MXQ_MXFP4) {
+                    tmem_st_x16(s_at + 32 * c, p);
+                    tmem_st_x16(s_at + 32 * c + 16, p + 16);
+                } else {
+                    tmem_st_x16(s_at + 16 * c, p);
+                }
             }
             if constexpr (QUAD) {  // the other warps' tokens
                 uint32_t z[16];
@@ -713,27 +738,6 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (c != quad) tmem_st_x16(s_at + 16 * c, z);
-            }
-            if constexpr (FMT == MXQ_MXFP4) {  // V's references of this tile; O follows where they moved
-                if (!wait_warp(&bar.vf[group], n >> 1 & 1u, a.status, 0x63)) {
-                    dead = true;
-                    break;
-                }
-                const int* refs = reinterpret_cast<const int*>(smem + C::OFF_REF) + (n & 3) * 4;
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    const int to = refs[b];
-                    if (begun && to != oref[b]) {  // the same for all threads
-                        const float f = scale_pow2(1.0f, max(oref[b] - to, -252));
-                        tmem_ld_32x32b_x32(o_at + 32 * b, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                        tmem_st_x16(o_at + 32 * b, v);
-                        tmem_st_x16(o_at + 32 * b + 16, v + 16);
-                    }
-                    oref[b] = to;
-                }
             }
             begun = true;
             tmem_st_wait();
@@ -812,10 +816,6 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
             }
         } else {
             // each group takes half of the channels
-            // (MXFP4: references of each group's last tile, written before its V was done and kept for four tiles)
-            const int* ref = reinterpret_cast<const int*>(smem + C::OFF_REF);
-            const int *ref0 = ref + ((last & 1) == 0 ? last & 3 : (last - 1) & 3) * 4,
-                      *ref1 = ref + ((last & 1) == 1 ? last & 3 : (last - 1) & 3) * 4;
             const float2 z0 = ml[tl], z1 = ml[128 + tl];
             const float most = fmaxf(z0.x, z1.x), f0 = has0 ? ex2(z0.x - most) : 0.0f, f1 = has1 ? ex2(z1.x - most) : 0.0f;
             const float sum = z0.y * f0 + z1.y * f1;
@@ -830,13 +830,13 @@ __device__ __forceinline__ void rows_softmax(const KvAttnArgs& a, uint8_t* smem,
                     tmem_ld_32x32b_x16(lanes + C::O_COL + d, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = value<FMT>(x[k], FMT == MXQ_MXFP4 ? ref0[d / 32] : 0) * f0;
+                    for (int k = 0; k < 16; ++k) y[k] = value<FMT>(x[k]) * f0;
                 }
                 if (has1) {
                     tmem_ld_32x32b_x16(lanes + C::O_COL + D + d, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = fmaf(value<FMT>(x[k], FMT == MXQ_MXFP4 ? ref1[d / 32] : 0), f1, y[k]);
+                    for (int k = 0; k < 16; ++k) y[k] = fmaf(value<FMT>(x[k]), f1, y[k]);
                 }
                 if (note.whole) {
                     if (real) {
@@ -880,14 +880,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) kv_attention_rows_kernel(const
             mbar_init(&bar.sf[i], 2);  // the products' end, and the issuing lane
             mbar_init(&bar.pf[i], kSoftWarps / 2);
             mbar_init(&bar.od[i], 1);
-            mbar_init(&bar.vm[i], kValueWarps);
             mbar_init(&bar.seg_full[i], 1);
             mbar_init(&bar.seg_empty[i], kSoftWarps + kDecWarps + 1);
         }
         mbar_init(bar.qf, 8);  // softmax warps or value warps
         fence_barrier_init();
     }
-    if (FMT == MXQ_MXFP4 && threadIdx.x < 16) reinterpret_cast<int*>(smem + C::OFF_MAX)[threadIdx.x] = 0;
     if (warp == kMmaWarp) {
         tmem_alloc(slot, 512);
         tmem_relinquish();

@@ -163,7 +163,7 @@ def test_large_scores(orc, fmt, D, G, q):
         assert (err <= tol).all(), "%g: off by %g of its tolerance" % (x, np.nanmax(err / np.maximum(tol, 1e-300)))
 
 
-@pytest.mark.parametrize("D,G,q", [s for s in SHAPES if s[0] == 256 or s[1] * s[2] <= 48])
+@pytest.mark.parametrize("D,G,q", SHAPES)
 @pytest.mark.parametrize("big,small", [(24, 0), (60, 0), (90, 0), (0, -60), (60, -40)])
 def test_mxfp4_values_of_any_scale(orc, D, G, q, big, small):
     """Values of 2^small beside ones of 2^big: tokens that a row does not see, and ones whose probability is 0, leave the
@@ -185,7 +185,7 @@ def test_mxfp4_values_of_any_scale(orc, D, G, q, big, small):
     kh.check_attention(out, lse, _reference(p, {0: [7, 100]}), "2^%d beside 2^%d" % (big, small))
 
 
-@pytest.mark.parametrize("D,G,q", [(64, 1, 3), (128, 5, 4), (256, 2, 3)])
+@pytest.mark.parametrize("D,G,q", [(64, 1, 3), (128, 5, 4), (256, 2, 3), (64, 1, 60), (128, 1, 70)])
 def test_mxfp4_values_that_are_no_numbers_stay_with_the_rows_that_see_them(orc, D, G, q):
     p = Problem("mxfp4", D, 1, G, 16, [90], [q], seed=12)
     pos = kh.positions(D, "mxfp4")
@@ -194,3 +194,18 @@ def test_mxfp4_values_that_are_no_numbers_stay_with_the_rows_that_see_them(orc, 
     p.cache[p.table[0, t // 16], :, 0, pos[3][t % 16]] = 0xFF
     out, lse = p.run(out_dtype=torch.float32)
     kh.check_attention(out[:-1], lse[:-1], tuple(x[:-1] for x in ref), "0xFF")
+
+
+@pytest.mark.parametrize("D,G,q", SHAPES)
+@pytest.mark.parametrize("exp", [30, 80])
+def test_mxfp4_keys_of_any_scale(orc, D, G, q, exp):
+    """Blocks of keys 2^exp above and below the others, under queries that are 0 there or as much smaller."""
+    n = 150
+    p = Problem("mxfp4", D, 1, G, 16, [n, 40], [q, 1], seed=D + q)
+    k = _rand((n, 1, D), 1)
+    k[::2, :, :32] = (k[::2, :, :32].double() * 2.0 ** exp).to(torch.bfloat16)
+    k[1::3, :, 32:] = (k[1::3, :, 32:].double() * 2.0 ** -exp).to(torch.bfloat16)
+    p.q[..., :32] = 0
+    _rewrite(p, k, _rand((n, 1, D), 2))
+    out, lse = p.run(out_dtype=torch.float32)
+    kh.check_attention(out, lse, p.ref(), "2^%d" % exp)
