@@ -326,7 +326,7 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
  *   info (device) int32[2]  info[0] = 0, or -1: a row outside the table, named twice or in an unfit state,
  *                           -2: a count or length that is negative or too long, -3: not enough free pages;
  *                           info[1] = the pages concerned (0 if refused).
- * Calls are stream-ordered and may be captured into a graph; n = 0 does nothing.
+ * Calls are stream-ordered and may be captured into a graph; n = 0 is such a call too: info becomes {0, 0}.
  */
 #define MXQ_KV_MAX_SEQS 4096
 #define MXQ_KV_MAX_TABLE 65536
@@ -336,8 +336,8 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
  * call's rows, and adds to kv_lens.  A last page that is not full and held by several rows is copied
  * first, in all layers, so that the others keep their tokens.  The cache is `layers` layers of
  * page_bytes = kv_heads * page_size / 16 * unit bytes a page, layer_stride bytes apart.
- *   slots  (device) int32 [slots_cap] or NULL: the slots of the new tokens, row after row, then -1.
- *   workspace (device) mxq_kv_reserve_workspace_size(n) bytes.   info[1] = pages taken.
+ *   slots  (device) int32 [slots_cap] or NULL: the slots of the new tokens, row after row, then -1 (all -1 if refused).
+ *   workspace (device) mxq_kv_reserve_workspace_size(n) bytes (n = 0: may be NULL).   info[1] = pages taken.
  */
 size_t mxq_kv_reserve_workspace_size(int64_t n);
 int mxq_kv_reserve(const int32_t* seqs, const int32_t* add, int64_t n, int32_t* block_table, int64_t table_rows,

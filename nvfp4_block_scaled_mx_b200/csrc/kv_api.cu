@@ -230,12 +230,11 @@ int mxq_kv_reserve(const int32_t* seqs, const int32_t* add, int64_t n, int32_t* 
     if (!aligned(seqs, 4) || !aligned(add, 4) || !aligned(slots, 4) || !aligned(workspace, 16)) return MXQ_ERR_ALIGN;
     if (n != 0 && ws_bytes < mxq_kv_reserve_workspace_size(n)) return MXQ_ERR_WORKSPACE;
     if ((rc = check_device()) != MXQ_OK) return rc;
-    if (n == 0) return MXQ_OK;
     KvPagesArgs a = pages_args(seqs, add, n, block_table, table_rows, table_stride, max_pages, kv_lens, refs, num_pages,
                                page_size, info);
     a.slots = slots;
     a.slots_cap = slots ? static_cast<int>(slots_cap) : 0;
-    a.pairs = static_cast<int32_t*>(workspace);
+    a.pairs = static_cast<int32_t*>(workspace);  // (n = 0 needs none)
     return launch_kv_reserve(a, static_cast<uint8_t*>(cache), layers, layer_stride, page_bytes,
                              reinterpret_cast<cudaStream_t>(stream));
 }
@@ -248,7 +247,6 @@ int mxq_kv_fork(const int32_t* parents, const int32_t* children, int64_t n, int3
     if (n != 0 && (!parents || !children)) return MXQ_ERR_NULL;
     if (!aligned(parents, 4) || !aligned(children, 4)) return MXQ_ERR_ALIGN;
     if ((rc = check_device()) != MXQ_OK) return rc;
-    if (n == 0) return MXQ_OK;
     return launch_kv_fork(pages_args(parents, children, n, block_table, table_rows, table_stride, max_pages, kv_lens, refs,
                                      num_pages, page_size, info),
                           reinterpret_cast<cudaStream_t>(stream));
@@ -262,7 +260,6 @@ int mxq_kv_truncate(const int32_t* seqs, const int32_t* new_lens, int64_t n, int
     if (n != 0 && (!seqs || !new_lens)) return MXQ_ERR_NULL;
     if (!aligned(seqs, 4) || !aligned(new_lens, 4)) return MXQ_ERR_ALIGN;
     if ((rc = check_device()) != MXQ_OK) return rc;
-    if (n == 0) return MXQ_OK;
     return launch_kv_truncate(pages_args(seqs, new_lens, n, block_table, table_rows, table_stride, max_pages, kv_lens, refs,
                                          num_pages, page_size, info),
                               reinterpret_cast<cudaStream_t>(stream));

@@ -300,7 +300,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) kv_reserv
     if (me == 0) {
         a.info[0] = code;
         a.info[1] = code < 0 ? 0 : static_cast<int>(want);
-        a.pairs[0] = code < 0 ? 0 : copies;
+        if (a.n > 0) a.pairs[0] = code < 0 ? 0 : copies;
     }
     if (code == 0 && want > 0)
         for (int p = p0; p < p1 && rank < want; ++p) {
@@ -461,7 +461,7 @@ int launch_kv_reserve(const KvPagesArgs& a, uint8_t* cache, int64_t layers, int6
         known[dev].store(1);
     }
     const int rc = launch(kv_reserve_kernel, kCluster, kThreads, sizeof(Reserve), st, a);
-    if (rc != MXQ_OK) return rc;
+    if (rc != MXQ_OK || a.n == 0) return rc;
     return launch(kv_move_kernel<false>, move_grid(a.n, layers, page_bytes), kCopyThreads, 0, st, a, cache, layers, layer_stride,
                   page_bytes, static_cast<const int*>(nullptr));
 }

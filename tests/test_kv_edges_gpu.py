@@ -209,3 +209,30 @@ def test_mxfp4_keys_of_any_scale(orc, D, G, q, exp):
     _rewrite(p, k, _rand((n, 1, D), 2))
     out, lse = p.run(out_dtype=torch.float32)
     kh.check_attention(out, lse, p.ref(), "2^%d" % exp)
+
+
+def test_page_calls_that_name_no_row(orc):
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    lens, refs = _dev([0, 0, 0]), _dev([0] * 6)
+    cache = torch.zeros(mxq.kv_cache_shape(6, 1, 64, "mxfp4", 16), dtype=torch.uint8, device="cuda")
+    none = _dev([])
+    state = (table, lens, refs)
+    slots = torch.empty(21, dtype=torch.int32, device="cuda")
+    assert mxq.kv_reserve(_dev([1]), _dev([20]), *state, cache, 16, slots=slots).tolist() == [0, 2]
+    before = [x.clone() for x in (*state, cache)]
+    for call in (lambda i: mxq.kv_reserve(none, none, *state, cache, 16, slots=slots, info=i),
+                 lambda i: mxq.kv_reserve(none, none, *state, cache, 16, info=i),
+                 lambda i: mxq.kv_fork(none, none, *state, 16, info=i),
+                 lambda i: mxq.kv_truncate(none, none, *state, 16, info=i)):
+        assert call(_dev([7, 7])).tolist() == [0, 0]
+        assert call(None).tolist() == [0, 0]
+    assert slots.tolist() == [-1] * 21  # an append that follows writes nothing
+    assert all(torch.equal(x, y) for x, y in zip((*state, cache), before)) and _status() == 0
+    # a captured call that names none
+    info = _dev([7, 7])
+    slots.fill_(3)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mxq.kv_reserve(none, none, *state, cache, 16, slots=slots, info=info)
+    g.replay()
+    assert info.tolist() == [0, 0] and slots.tolist() == [-1] * 21
