@@ -258,7 +258,8 @@ int mxq_linear_noalloc(const void* x_bf16, const void* W_q, const uint8_t* W_sf,
  * Sequence b's token p lies in page block_table[b][p / page_size].
  * The kernels check what they read on the device before they use it as an index.  What they find out of
  * range is skipped and recorded in the device status word (mxq_device_status), first finding first:
- * 0x200 a slot, 0x201 a page of the block table, 0x202 q_start, 0x203 a length the table cannot hold.
+ * 0x200 a slot, 0x201 a page of the block table, 0x202 q_start (outside q, falling, or more than max_q rows: the sequence
+ * gets none), 0x203 a length the table cannot hold (the sequence has what the table holds).  A negative length is 0.
  */
 
 /* Bytes of one unit (16 tokens of one head). */

@@ -50,7 +50,7 @@ inline int kv_unit_bytes(int head_dim, int fmt) { return 16 * head_dim + 32 * (h
 // Status codes of the key/value cache kernels in the device status word (first writer wins).
 constexpr int kStatusKvSlot = 0x200;   // a slot at or behind num_pages * page_size
 constexpr int kStatusKvPage = 0x201;   // a block-table entry outside the cache
-constexpr int kStatusKvRows = 0x202;   // q_start outside q, or more than max_q rows
+constexpr int kStatusKvRows = 0x202;   // q_start outside q or falling, or more than max_q rows
 constexpr int kStatusKvLen = 0x203;    // a length that the block table cannot hold
 
 __device__ __forceinline__ void kv_status(int* status, int code) { atomicCAS(status, 0, code); }

@@ -36,7 +36,7 @@ __device__ __noinline__ Seq load_seq(const KvAttnArgs& a, int b) {
     s.kv = min(max(kv, 0), a.max_len);
     s.q0 = q0;
     s.qn = max(q1 - q0, 0);
-    const bool bad_rows = q0 < 0 || q1 > a.rows_total || s.qn > a.max_q;
+    const bool bad_rows = q0 < 0 || q1 < q0 || q1 > a.rows_total || s.qn > a.max_q;
     if (bad_rows) s.q0 = s.qn = 0;
     if (bad_rows || kv > a.max_len) kv_status(a.status, bad_rows ? kStatusKvRows : kStatusKvLen);
     return s;

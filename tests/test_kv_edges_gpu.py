@@ -236,3 +236,12 @@ def test_page_calls_that_name_no_row(orc):
         mxq.kv_reserve(none, none, *state, cache, 16, slots=slots, info=info)
     g.replay()
     assert info.tolist() == [0, 0] and slots.tolist() == [-1] * 21
+
+
+@pytest.mark.parametrize("max_q", [3, 40])
+def test_starts_that_fall_are_reported(orc, max_q):
+    p = Problem("nvfp4", 128, 1, 1, 16, [40, 33], [3, 3], seed=14)
+    want = p.run(max_q=max_q)[0]
+    out, _ = mxq.kv_attention(p.q.cuda(), torch.from_numpy(p.cache).cuda(), _dev(p.table), _dev(p.lens), "nvfp4",
+                              q_start=_dev([0, 3, 2]), max_q=max_q, g_k=p.dk, g_v=p.dv)
+    assert _status() == 0x202 and torch.equal(out[:3], want[:3])
