@@ -492,14 +492,17 @@ def kv_attention_workspace(batch, max_q, heads, kv_heads, head_dim):
     return lib().mxq_kv_attention_workspace_size(batch, max_q, heads, kv_heads, head_dim)
 
 
-def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, scale=None, causal=True, window=0, g_k=None,
+def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=None, scale=None, causal=True, window=0, g_k=None,
                  g_v=None, out_dtype=torch.bfloat16, out=None, lse=None, workspace=None, stream=None):
     """Attention of q [rows, heads, dim] bf16 (strided) over one layer of the cache: (out [rows, heads, dim],
     lse [rows, heads] fp32, natural logarithm).
 
     block_table int32 [batch, pages], kv_lens int32 [batch] (the query tokens included), q_start int32
-    [batch + 1] (None: max_q rows a sequence).  scale: dim ** -0.5 by default.  Rows that see no token
-    get zeros and -inf; rows of no sequence are left as they were."""
+    [batch + 1] (None: max_q rows a sequence, 1 by default).  With q_start, max_q is the most rows that any sequence
+    may have; None takes all of q's, which is always right, but a batch of one or few rows each is faster with its own
+    bound (kernel and workspace go by it).  scale: dim ** -0.5 by default.  Rows that see no token get zeros and
+    -inf; rows of no sequence, and of one with more than max_q, are left as they were (what the call allocates
+    itself holds anything there), the latter recorded in mxq_device_status."""
     f, dev = _fmt(fmt), q.device
     if q.dim() != 3 or block_table.dim() != 2:
         raise MxqBufferError("q must be [rows, heads, dim] and block_table [batch, pages] (got %s, %s)" %
@@ -508,6 +511,8 @@ def kv_attention(q, cache, block_table, kv_lens, fmt, q_start=None, max_q=1, sca
     pages, kv_heads, page_size = _kv_layer(cache, D, f)
     qp, qs, qh = _rows(q, "q", dev)
     batch, cols = block_table.shape
+    if max_q is None:
+        max_q = 1 if q_start is None else max(rows, 1)
     t0, t1 = block_table.stride()
     if (t1 != 1 and cols > 1) or block_table.dtype is not _I32 or block_table.device != dev:
         raise MxqBufferError("block_table must be torch.int32 [batch, pages] with contiguous rows, on the call's device")

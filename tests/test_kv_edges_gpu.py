@@ -238,6 +238,14 @@ def test_page_calls_that_name_no_row(orc):
     assert info.tolist() == [0, 0] and slots.tolist() == [-1] * 21
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 5), (256, 2)])
+def test_query_rows_without_a_bound(orc, fmt, D, G):
+    p = Problem(fmt, D, 2, G, 16, [100, 33, 0, 70], [3, 0, 2, 30], seed=D)
+    out, lse = p.run(max_q=None)
+    kh.check_attention(out, lse, p.ref(), fmt)
+
+
 @pytest.mark.parametrize("max_q", [3, 40])
 def test_starts_that_fall_are_reported(orc, max_q):
     p = Problem("nvfp4", 128, 1, 1, 16, [40, 33], [3, 3], seed=14)
