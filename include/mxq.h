@@ -293,9 +293,10 @@ size_t mxq_kv_attention_workspace_size(int64_t batch, int64_t max_q, int heads, 
  * scale * q_i . K_p, for heads = kv_heads * group query heads (head h reads kv head h / group).
  *   q            (device) [rows, heads, D] bf16; element strides q_token_stride, q_head_stride, multiples
  *                of 8; the innermost dimension contiguous.
- *   block_table  (device) int32 [batch][table_stride], the first max_pages columns used; entries behind a
- *                sequence's last page are not read.  kv_lens (device) int32 [batch]: tokens in the cache,
- *                the query tokens' own included.
+ *   block_table  (device) int32 [batch][table_stride], the first max_pages columns used; entries of pages
+ *                without a token that some row of the sequence sees (behind its last, in front of all windows)
+ *                are not read.  kv_lens (device) int32 [batch]: tokens in the cache, the query tokens' own
+ *                included.
  *   q_start      (device) int32 [batch + 1]: sequence b's query rows are q_start[b] .. q_start[b + 1] - 1,
  *                at most max_q; NULL: max_q rows each, rows = batch * max_q.
  *   causal       query j of a sequence's n sees the tokens up to its own, kv_lens[b] - n + j; 0: all.

@@ -601,14 +601,15 @@ __device__ __forceinline__ void feed(const KvAttnArgs& a, uint8_t* smem) {
         constexpr int BATCH = 8;
         static_assert(BATCH <= C::STAGES, "a slot comes up once in a batch: its barrier has one parity bit");
         const int first_unit = (t0 + from) * C::TU;
-        const int units_end = min((seen1 + 15) >> 4, first_unit + count * C::TU);  // behind the tokens pages may not exist
+        // In front of and behind the tokens that some row sees, pages may not exist (a window's may have been given away)
+        const int units_from = seen0 >> 4, units_end = min((seen1 + 15) >> 4, first_unit + count * C::TU);
         int page[C::TU], in_page[C::TU];  // of the lane's units of the next batch; page is not looked at before it is used
         auto look_up = [&](int tile) {    // for the batch that begins at `tile`
 #pragma unroll
             for (int u = 0; u < C::TU; ++u) {
                 const int unit = first_unit + (tile + lane) * C::TU + u;
                 const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));  // unit / page_units
-                in_page[u] = lane < BATCH && unit < units_end ? unit - at_page * a.page_units : -1;
+                in_page[u] = lane < BATCH && unit >= units_from && unit < units_end ? unit - at_page * a.page_units : -1;
                 page[u] = 0;
                 if (in_page[u] >= 0) page[u] = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             }

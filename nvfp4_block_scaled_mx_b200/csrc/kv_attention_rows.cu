@@ -202,10 +202,11 @@ __device__ __forceinline__ void rows_feed(const KvAttnArgs& a, uint8_t* smem, co
             mbar_arrive(&bar.seg_full[buf]);
         }
         const int first_unit = (t0 + from) * C::UNITS;
-        const int units_end = min((seen1 + 15) >> 4, first_unit + count * C::UNITS);  // behind the tokens pages may not exist
+        // In front of and behind the tokens that some row sees, pages may not exist (a window's may have been given away)
+        const int units_from = seen0 >> 4, units_end = min((seen1 + 15) >> 4, first_unit + count * C::UNITS);
         auto source_of = [&](int i) -> int64_t {  // of the lane's unit of tile i; not loaded: -1, and -2 where the page is none of the cache's
             const int unit = first_unit + i * C::UNITS + lane;
-            if (lane >= C::UNITS || unit >= units_end) return -1;
+            if (lane >= C::UNITS || unit < units_from || unit >= units_end) return -1;
             const int at_page = a.page_units == 1 ? unit : static_cast<int>(__umulhi(unit, a.page_magic));
             const int pg = a.table[static_cast<int64_t>(b) * a.table_stride + at_page];
             if (pg < 0 || pg >= a.num_pages) {

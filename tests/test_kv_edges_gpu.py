@@ -253,3 +253,16 @@ def test_starts_that_fall_are_reported(orc, max_q):
     out, _ = mxq.kv_attention(p.q.cuda(), torch.from_numpy(p.cache).cuda(), _dev(p.table), _dev(p.lens), "nvfp4",
                               q_start=_dev([0, 3, 2]), max_q=max_q, g_k=p.dk, g_v=p.dv)
     assert _status() == 0x202 and torch.equal(out[:3], want[:3])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G,q", SHAPES)
+def test_pages_in_front_of_the_window_are_not_looked_at(orc, fmt, D, G, q):
+    """A page all of whose tokens lie in front of every row's window may have been given to others."""
+    p = Problem(fmt, D, 2, G, 16, [300, 64, 17, 233], [q, 1, 1, q], seed=D + q)
+    want = p.run(window=20)
+    for b, n in enumerate(p.lens):
+        first = max(n - int(p.q_start[b + 1] - p.q_start[b]) + 1 - 20, 0)
+        p.table[b, :first // 16] = -7
+    out, lse = p.run(window=20)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
