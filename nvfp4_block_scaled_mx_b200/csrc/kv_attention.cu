@@ -14,7 +14,7 @@
 // f16 but for elements 2^-24 below the row's largest.  V: the scale multiplies P instead of the codes,
 // in f16: P is rounded to 11 bits (a bf16 P, 8 bits, would add as much error as the bf16 output has),
 // times 2^7 (NVFP4) or 2^4 (MXFP4) so that small probabilities keep their bits.  MXFP4 scales are taken relative to a
-// reference per 32 channels, the largest one met so far; a tile with scales that f16 does not hold beside it goes
+// reference per 32 channels; a tile with scales that f16 does not hold beside it goes
 // another way (wide_step), band by band of 16 codes, so that no value is lost beside another, seen or not.
 // Sums, maxima and accumulators are fp32.
 //
@@ -83,13 +83,14 @@ struct Warp {
     using C = Cfg<FMT, D, NT>;
     float o[NT][C::KS][4];
     float base[NT][2], l[NT][2];  // probabilities are 2^(cs (s - base) + SHIFT): base is the running maximum of s
-    // MXFP4, per 32 channels: E8M0 code that stands for 2^9 in the factors and in O, the largest met within kRefMin and
-    // kRefMax.  (O is fp32 in units of 2^(ref - 136): it must not overflow beside values of 2^127, nor vanish beside
-    // a reference that follows them up; so values of 2^-90 keep their bits beside any.)
+    // MXFP4, per 32 channels: E8M0 code that stands for 2^9 in the factors and in O.  It begins at 2^0, where most values'
+    // scales are near, and follows a tile's largest code, within kRefMin and kRefMax, where that lies outside the band.  (O is
+    // fp32 in units of 2^(ref - 136): it must not overflow beside values of 2^127, nor vanish beside a reference that
+    // follows them up; so values of 2^-90 keep their bits beside any, and a reference above kRefDown stays.)
     int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];
     uint32_t bias;  // 13 - ref of the two blocks whose scales the lane checks, one a half
 };
-constexpr int kRefMin = 127 - 40, kRefMax = 127 + 40;
+constexpr int kRefMin = 127 - 40, kRefMax = 127 + 40, kRefDown = 127 + 20;
 // Scales that go into one product: codes ref - 13 to ref + 2, so factors 2^-4 to 2^11; with P of 2^4 at most the
 // product keeps f16's bits down to P = 2^-10, and holds the largest.
 constexpr int kBand = 16;
@@ -108,8 +109,8 @@ __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
     }
     if constexpr (FMT == MXQ_MXFP4) {
 #pragma unroll
-        for (int b = 0; b < C::U::NB; ++b) w.ref[b] = -1000;
-        w.bias = 1013u * 0x10001u;
+        for (int b = 0; b < C::U::NB; ++b) w.ref[b] = 127;
+        w.bias = static_cast<uint32_t>((13 - 127) & 0xFFFF) * 0x10001u;
     }
 }
 
@@ -237,8 +238,8 @@ struct Scales {
     }
     __device__ __forceinline__ bool odd(const Warp<MXQ_MXFP4, D, NT>& w) const { return ((place(0, w) | place(1, w)) & 0xFFF0FFF0u) != 0; }
 
-    // Moves the references (and O) up to the tile's scales where those pass them; whether scales remain that do not go
-    // into one product.
+    // Moves the references (and O) to the tile's largest scales where those lie outside the bands; whether scales remain
+    // that do not go into one product.
     __device__ __forceinline__ bool refer(Warp<MXQ_MXFP4, D, NT>& w) const {
         uint32_t most = __vmaxu2(codes(0), codes(1));
 #pragma unroll
@@ -246,8 +247,8 @@ struct Scales {
 #pragma unroll
         for (int b = 0; b < U::NB; ++b) {
             const int code = __shfl_sync(0xffffffffu, most, b >> 1) >> (16 * (b & 1)) & 0xFFFF, to = min(max(code, kRefMin), kRefMax);
-            if (code > w.ref[b] + 2 && to > w.ref[b]) {
-                const float f = scale_pow2(1.0f, max(w.ref[b] - to, -252));
+            if (code > w.ref[b] + 2 || (code != 0 && code < w.ref[b] + 3 - kBand && w.ref[b] <= kRefDown)) {
+                const float f = __uint_as_float(static_cast<uint32_t>(w.ref[b] - to + 127) << 23);
                 w.ref[b] = to;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     x[k] = w.o[i][j][k];
-                    if constexpr (FMT == MXQ_MXFP4) x[k] = scale_pow2(x[k], max(w.ref[j / 2], 0) - 136);
+                    if constexpr (FMT == MXQ_MXFP4) x[k] = scale_pow2(x[k], w.ref[j / 2] - 136);
                 }
                 float* dst = red + (warp * C::ROWS + 8 * i + 2 * t) * C::OSTRIDE + 16 * j + 2 * g;
                 *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[2]);

@@ -164,7 +164,7 @@ def test_large_scores(orc, fmt, D, G, q):
 
 
 @pytest.mark.parametrize("D,G,q", SHAPES)
-@pytest.mark.parametrize("big,small", [(24, 0), (60, 0), (90, 0), (0, -60), (60, -40)])
+@pytest.mark.parametrize("big,small", [(24, 0), (60, 0), (90, 0), (0, -60), (60, -40), (110, 0), (100, -80)])
 def test_mxfp4_values_of_any_scale(orc, D, G, q, big, small):
     """Values of 2^small beside ones of 2^big: tokens that a row does not see, and ones whose probability is 0, leave the
     others' values as they are.  In every second block of 32 channels the large values are elsewhere."""
