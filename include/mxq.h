@@ -304,14 +304,16 @@ size_t mxq_kv_attention_workspace_size(int64_t batch, int64_t max_q, int heads, 
  *   g_k, g_v     (device) fp32[1] NVFP4 global scales; ignored (may be NULL) for MXFP4.
  *   out          (device) [rows, heads, D] bf16 (RNE) or fp32.  lse (device) fp32 [rows, heads], the natural
  *                logarithm of the softmax's denominator, or NULL.  A row that sees no token gets zeros and
- *                -inf.  Rows of no sequence are left as they were.
+ *                -inf.  Rows of no sequence are left as they were.  Neither overlaps an input.
  *   workspace    (device) at least mxq_kv_attention_workspace_size(...) bytes; needs no preparation.
- * max_pages * page_size <= 2^30 - 1024.  Scores, softmax and sums are fp32.  Rounded to fewer bits are q, to 2^-32 of its
- * row's largest element (MXFP4 with many rows: not at all), and probabilities, for the product with V, to f16: 2^-11 of
- * one, or 2^-28 of the row's largest where that is more; with few rows their product with V's scale once more so; MXFP4
- * with many rows keeps 16 bits.  MXFP4 values below 2^-90 and blocks of scale byte 0 may count as zero.  Scale bytes that
- * are not numbers, which the quantizer never writes, have an effect on rows that see the token alone.  Results do not
- * depend on timing.  Two launches.  Calls that may run at the same time need a workspace each.
+ * max_pages * page_size <= 2^30 - 1024.  Scores, softmax and sums are fp32.  Rounded to fewer bits are q, to 2^-32
+ * of its row's largest element (MXFP4 with many rows: not at all), and probabilities, for the product with V, to
+ * f16: 2^-11 of one, or 2^-28 of the row's largest where that is more; with few rows their product with V's scale
+ * once more so; MXFP4 with many rows keeps 16 bits.  ("Many": more than 16 rows a sequence and kv head for NVFP4
+ * with heads of 128, 48 else; never with heads of 256.)  MXFP4 keys and values below 2^-90 and blocks of scale byte
+ * 0 may count as zero.  Scale bytes that are not numbers, which the quantizer never writes, have an effect on
+ * rows that see the token alone.  Results do not depend on timing.  Two launches.  Calls that may run at the same
+ * time need a workspace each.
  */
 int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
                      int64_t num_pages, int page_size, int heads, int kv_heads, int head_dim, mxq_fmt fmt,
@@ -335,9 +337,11 @@ int mxq_kv_attention(const void* q, int64_t rows, int64_t q_token_stride, int64_
 
 /*
  * Room for add[i] more tokens in row seqs[i]: takes free pages, lowest index first in the order of the
- * call's rows, and adds to kv_lens.  A last page that is not full and held by several rows is copied
- * first, in all layers, so that the others keep their tokens.  The cache is `layers` layers of
- * page_bytes = kv_heads * page_size / 16 * unit bytes a page, layer_stride bytes apart.
+ * call's rows, and adds to kv_lens.  A last page that is not full and held by several rows (refs > 1 in front
+ * of the call) is copied first, in all layers, so that the others keep their tokens.  That holds for each of the
+ * call's rows: where it names all holders of a page, all of them copy it and the page becomes free, so that until
+ * then one page more is taken (and -3 answered where it is missing) than the rows need.  The cache is `layers`
+ * layers of page_bytes = kv_heads * page_size / 16 * unit bytes a page, layer_stride bytes apart.
  *   slots  (device) int32 [slots_cap] or NULL: the slots of the new tokens, row after row, then -1 (all -1 if refused).
  *   workspace (device) mxq_kv_reserve_workspace_size(n) bytes (n = 0: may be NULL).   info[1] = pages taken.
  */

@@ -25,9 +25,9 @@
 //
 // What bounds it: beginning (5 us from the dependency to a CTA's first tile: lengths, page numbers and tiles, one
 // round trip each), then about 5 TB/s of tiles (ALU pipe 50 % busy; the three CTAs of an SM come forward unequally,
-// equal shares end up to 10 us apart), then the join (5 us).  40 heads, 8 kv heads of 128: one sequence of 131061 (NVFP4, 151 MB) 43.5 us, 32
-// sequences of 500 to 16000 (MXFP4, 161 MB) 49.6 us, one of 1009 11.7 us; 24 heads, 4 kv heads of 256, a window
-// of 2048 over 24 sequences of 90 to 9000 (MXFP4, 29 MB) 24.7 us.
+// equal shares end up to 10 us apart), then the join (5 us).  40 heads, 8 kv heads of 128: one sequence of 131061 (NVFP4, 151 MB) 43.9 us, 32
+// sequences of 500 to 16000 (MXFP4, 161 MB) 51.5 us, one of 1009 12.0 us; 24 heads, 4 kv heads of 256, a window
+// of 2048 over 24 sequences of 90 to 9000 (MXFP4, 29 MB) 25.1 us.
 #include <algorithm>
 #include <atomic>
 
@@ -39,8 +39,8 @@ namespace {
 
 constexpr int kWarps = 4;                     // warps that compute; one more feeds them
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kMinTiles = 4;     // token tiles a CTA gets at least (4 of 4, 8 and 12: 11.6, 12.0, 12.4 us for one sequence of 1009)
-constexpr int kExtraTiles = 10;  // counted for beginning a row tile (32 sequences of 500 to 16000: 56.6 us at 0, 51.3 at 6, 49.4 at 10)
+constexpr int kMinTiles = 4;     // token tiles a CTA gets at least (4, 8 and 12: 11.9, 12.9, 12.0 us for one sequence of 1009, MXFP4 12.1, 13.2, 12.5)
+constexpr int kExtraTiles = 10;  // counted for beginning a row tile (32 sequences of 500 to 16000, MXFP4: 59.0 us at 0, 53.3 at 6, 51.5 at 10, 51.6 at 14)
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -323,8 +323,8 @@ __device__ __forceinline__ void wide_values(Warp<MXQ_MXFP4, D, NT>& w, const uin
 
 // One token tile: scores, softmax update, O update.  pos0 is the tile's first token; MASK: some row does
 // not see all of its tokens; seen0 / seen1: tokens that any row of the tile sees; skip: units that no row sees.  False for a
-// tile of MXFP4 with V scales far apart, which has to be taken again with WIDE.  (One copy of the code
-// with branches in it took 75 us where the two take 65: the branches part what the scheduler interleaves.)
+// tile of MXFP4 with V scales far apart, which has to be taken again with WIDE.  (Two
+// copies of the code: with MASK for every tile 32 sequences take 75 to 84 us where they take 50 to 52.)
 template <int FMT, int D, int NT, bool MASK, bool WIDE = false>
 __device__ __forceinline__ bool tile_step(Warp<FMT, D, NT>& w, uint32_t tile, uint32_t qf, const float (&cs)[NT][2],
                                           const int* row_first, const int* row_end, int pos0, int seen0, int seen1, uint32_t skip) {
@@ -915,18 +915,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::CTAS) kv_attention_
 // --------------------------------------------------------------------------------------- host
 
 // n-tiles of eight rows a CTA takes at once, one or two: the second one costs 3/4 of the first (head size 256: 8/9), as
-// K and V are decoded already, but the last row tile pads to 16 rows.  Head size 128, NVFP4: 20 rows 55 us with
-// one, 54 with two; 35 rows 82 and 75; head size 256: 10 rows 71 and 66, 20 rows 100 and 118, 500 rows 1814 and
-// 1618.  Three or four leave room for half the warps (MXFP4, a chunk of 700 tokens: 772 us with two, 855 and 817).
+// K and V are decoded already, but the last row tile pads to 16 rows.  16 sequences of 3000 to 4100, with one and
+// with two, in us: head size 128, MXFP4, 10 rows 42 and 37, 20 rows 56 and 58, 35 rows 83 and 80; 64, 10 rows 31 and 28,
+// 35 rows 57 and 52; head size 256, 10 rows 71 and 69, 20 rows 99 and 124, 50 rows 210 and 228, 500 rows 1745 and 1685.
+// Three or four leave room for half the warps (slower by 6 to 11 % for a chunk of 700 tokens).
 int n_tiles(int64_t rows, int D) {
     const int64_t ones = (rows + 7) / 8, twos = 2 * ((rows + 15) / 16);
     return (D == 256 ? 9 * ones < 8 * twos : ones == 1) ? 1 : 2;
 }
 
 // Rows from which a row tile on tcgen05 (32 rows for NVFP4 with head size 128, else 128) takes less time.  16
-// sequences of 3000 to 4100, 8 kv heads, here and there, in us: NVFP4, 128 wide, 10 rows 35 and 47, 20 rows 54 and
-// 48, 65 rows 115 and 75; 64 wide, 35 rows 50 and 61, 65 rows 73 and 62; MXFP4, 128 wide, 35 rows 79 and 99, 65 rows
-// 122 and 101, 500 rows 688 and 302; 64 wide, 35 rows 51 and 75, 65 rows 76 and 76, 500 rows 402 and 231.
+// sequences of 3000 to 4100, 8 kv heads, here and there, in us: NVFP4, 128 wide, 10 rows 35 and 47, 20 rows 55 and
+// 48, 35 rows 76 and 71, 65 rows 117 and 73; 64 wide, 35 rows 51 and 58, 50 rows 63 and 59, 65 rows 75 and 59; MXFP4, 128
+// wide, 35 rows 80 and 85, 50 rows 102 and 86, 65 rows 123 and 87, 500 rows 689 and 254; 64 wide, 35 rows 51 and 66, 50
+// rows 64 and 67, 65 rows 76 and 67, 500 rows 397 and 201.
 bool on_tcgen05(int fmt, int D, int64_t rows) {
     return D <= 128 && rows > (fmt == MXQ_NVFP4 && D == 128 ? 16 : 48);
 }

@@ -10,28 +10,29 @@
 //   O += P V    V codes times scale in shared memory, transposed ([channel][token]).
 // NVFP4 operands are f16, which holds codes times E4M3 scales exactly, and P rounded to 11 bits.  MXFP4 operands are bf16:
 // codes times E8M0 scales need two bits and the whole range of exponents, which f16 does not have.  (As f16 relative to a
-// running reference, blocks 2^23 below it vanished, and eight warps agreed on that reference in every tile: a chunk of 700
-// took 310 us.)  P is two bf16 then, its upper and its lower 8 bits, and O two products.
+// running reference, blocks 2^23 below it vanished, and eight warps agreed on that reference in every tile: 5 % slower.)
+// P is two bf16 then, its upper and its lower 8 bits, and O two products.
 // Roles: two groups of 4 softmax warps (their TMEM lanes are the rows) that take the tiles in turn, each with
 // its own S and O, so that one group's exponentials run beside the other's products; 4 warps that decode K
 // (32 tokens of a tile each) and 8 that decode V (16 tokens); one warp that feeds raw tiles by bulk copies;
-// one that issues the MMAs.  P takes the place of S's first half: chunk by chunk of 32 tokens the scores are
+// one that issues the MMAs.  P takes the place of S, of its first half as f16: chunk by chunk of 32 tokens the scores are
 // read, and their probabilities written where scores have been read already.
-// QUAD (NVFP4, up to 32 rows): the rows stand four times in the lanes, and each softmax warp takes 32 of the tile's
-// 128 tokens, the others' P columns being zero: the four partial results join at the end, like CTAs' parts.
+// QUAD (up to 32 rows): the rows stand four times in the lanes, and each softmax warp takes 32 of the tile's 128
+// tokens, the others' P columns being zero: the four partial results join at the end, like CTAs' parts.  NVFP4 with heads
+// of 128 alone: 20 rows of MXFP4 took 80 us so and 55 in kv_attention.cu, and heads of 64 take 38 there.
 // The base of a row follows its maximum only when a probability would pass 2^15 (f16 ends at 2^16); O and
 // the tile's earlier P are rescaled in TMEM then.  Work is cut over the CTAs as in kv_attention.cu, with the
 // same join kernel.
 //
-// What bounds it: a tile takes 2200 to 2500 cycles.  The products alone take 1750: eight instructions of S and of
+// What bounds it (NVFP4): a tile takes 2200 to 2500 cycles.  The products alone take 1750: eight instructions of S and of
 // P V are issued in 870 cycles each, not the 512 of an idle SM, as K, V and Q are read from shared memory beside the
 // decoders' writes (about 200 KB a tile at 128 bytes a cycle).  A softmax group of 128 rows needs 3600 cycles for
 // 128 scores a thread, two groups in turn.  Beside that a segment ends in 5000 to 10000 cycles (the last product,
 // joining the groups); with Q brought by the softmax warps afterwards, not by the value warps meanwhile, a chunk took
 // 11 us more.  Giving raw tiles back before the wait for the operand's place changed nothing.
-// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 195 us for NVFP4
-// (582 TFLOP/s), 279 for MXFP4, whose value warps also agree on references tile by tile.  Four drafted tokens for
-// each of 16 sequences of 3000 to 4100: 48 us.
+// A chunk of 700 tokens over 2 sequences of 4200 to 8300 (40 heads, 8 kv heads of 128): 194 us for NVFP4
+// (583 TFLOP/s), 242 for MXFP4, whose P V is two products.  Four drafted tokens for each of 16 sequences of 3000 to
+// 4100 (NVFP4): 49 us.
 #include <algorithm>
 #include <atomic>
 
@@ -53,8 +54,8 @@ template <int FMT, int D, bool QUAD>
 struct RCfg {
     using U = KvUnit<FMT, D>;
     static constexpr int ROWS = QUAD ? 32 : 128;
-    // Tiles counted for beginning a row tile: a chunk of 700 takes 196 us at 3, 195 at 5, 198 at 8, 206 at 12; four drafted
-    // tokens 48.8 at 5, 48.7 at 8, 48.3 at 12, 49.4 at 16.
+    // Tiles counted for beginning a row tile: a chunk of 700 takes 195 us at 3 and 5, 201 at 8, 208 at 12 (MXFP4 239,
+    // 242, 250, 259); four drafted tokens 49.6 at 5, 49.5 at 8, 49.0 at 12, 50.0 at 16.
     static constexpr int EXTRA = QUAD ? 12 : 5;
     static constexpr int UNITS = kTokens / 16;
     static constexpr int RAW = UNITS * U::BYTES;
