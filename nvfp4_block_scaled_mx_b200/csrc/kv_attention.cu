@@ -15,7 +15,7 @@
 // in f16: P is rounded to 11 bits (a bf16 P, 8 bits, would add as much error as the bf16 output has),
 // times 2^7 (NVFP4) or 2^4 (MXFP4) so that small probabilities keep their bits.  MXFP4 scales are taken relative to a
 // reference per 32 channels; a tile with scales that f16 does not hold beside it goes
-// another way (wide_step), band by band of 16 codes, so that no value is lost beside another, seen or not.
+// another way (wide_step), band by band of 12 codes, so that no value is lost beside another, seen or not.
 // Sums, maxima and accumulators are fp32.
 //
 // Work is the list of all (sequence, row tile, kv head, token tile), cut evenly over the CTAs by every
@@ -88,12 +88,13 @@ struct Warp {
     // fp32 in units of 2^(ref - 136): it must not overflow beside values of 2^127, nor vanish beside a reference that
     // follows them up; so values of 2^-90 keep their bits beside any, and a reference above kRefDown stays.)
     int ref[FMT == MXQ_MXFP4 ? C::U::NB : 1];
-    uint32_t bias;  // 13 - ref of the two blocks whose scales the lane checks, one a half
+    uint32_t bias;  // kBand - 3 - ref of the two blocks whose scales the lane checks, one a half
 };
 constexpr int kRefMin = 127 - 40, kRefMax = 127 + 40, kRefDown = 127 + 20;
-// Scales that go into one product: codes ref - 13 to ref + 2, so factors 2^-4 to 2^11; with P of 2^4 at most the
-// product keeps f16's bits down to P = 2^-10, and holds the largest.
-constexpr int kBand = 16;
+// Scales that go into one product: codes ref - 9 to ref + 2, so factors 2^0 to 2^11.  P of 2^4 at most times the largest
+// fits f16; below f16's normal range P is off by 2^-25 and its product by as much, together 2^-28 of the largest
+// probability times the row's own largest value, whatever the reference follows.
+constexpr int kBand = 12;
 
 template <int FMT, int D, int NT>
 __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
@@ -110,7 +111,7 @@ __device__ __forceinline__ void warp_reset(Warp<FMT, D, NT>& w) {
     if constexpr (FMT == MXQ_MXFP4) {
 #pragma unroll
         for (int b = 0; b < C::U::NB; ++b) w.ref[b] = 127;
-        w.bias = static_cast<uint32_t>((13 - 127) & 0xFFFF) * 0x10001u;
+        w.bias = static_cast<uint32_t>((kBand - 3 - 127) & 0xFFFF) * 0x10001u;
     }
 }
 
@@ -213,7 +214,7 @@ __device__ __forceinline__ void scores(uint32_t tile, uint32_t qf, float (&s)[Cf
     }
 }
 
-// MXFP4, the V scales of a tile: a lane looks at four bytes, of a pair of tokens and two blocks (ten instructions a tile).
+// MXFP4, the V scales of a tile: a lane looks at four bytes, of a pair of tokens and two blocks (a dozen instructions a tile).
 template <int D, int NT>
 struct Scales {
     using C = Cfg<MXQ_MXFP4, D, NT>;
@@ -231,12 +232,16 @@ struct Scales {
         const int u = word() / (4 * U::NB);
         x[0] &= skip >> u & 1u ? 0u : pair_mask(pos0 + 16 * u + word() % (4 * U::NB) / PER * 2, seen0, seen1);
     }
-    // either token's codes, a block a half, and code - ref + 13, in [0, 16) if all is well (negative: a large unsigned one)
+    // either token's codes, a block a half, and code - ref + kBand - 3, in [0, kBand) if all is well (negative: a large unsigned one)
     __device__ __forceinline__ uint32_t codes(int token) const { return prmt(x[0], 0u, token ? 0x4341u : 0x4240u); }
     __device__ __forceinline__ uint32_t place(int token, const Warp<MXQ_MXFP4, D, NT>& w) const {
         return __viaddmax_s16x2(codes(token), w.bias, 0x80008000u);
     }
-    __device__ __forceinline__ bool odd(const Warp<MXQ_MXFP4, D, NT>& w) const { return ((place(0, w) | place(1, w)) & 0xFFF0FFF0u) != 0; }
+    __device__ __forceinline__ bool odd(const Warp<MXQ_MXFP4, D, NT>& w) const {
+        const uint32_t most = __vmaxu2(place(0, w), place(1, w));
+        // (a carry into the upper half comes from a lower one that is odd itself)
+        return (((most + (0x8000u - kBand) * 0x10001u) | most) & 0x80008000u) != 0;
+    }
 
     // Moves the references (and O) to the tile's largest scales where those lie outside the bands; whether scales remain
     // that do not go into one product.
@@ -257,7 +262,7 @@ struct Scales {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) w.o[n][j][i] *= f;
             }
-            const uint32_t half = static_cast<uint32_t>(13 - w.ref[b]) & 0xFFFFu;
+            const uint32_t half = static_cast<uint32_t>(kBand - 3 - w.ref[b]) & 0xFFFFu;
             if (which() == b >> 1) w.bias = b & 1 ? (w.bias & 0xFFFFu) | half << 16 : half;
         }
         // (code 0 counts as 0: the quantizer writes it for zeros, and for what is below 2^-124)
@@ -268,7 +273,7 @@ struct Scales {
     }
 };
 
-// O += V^T P^T of one unit in bands of 16 codes: each product from zero, added to O in fp32 times the band's power of two.
+// O += V^T P^T of one unit in bands of kBand codes: each product from zero, added to O in fp32 times the band's power of two.
 template <int D, int NT>
 __device__ __forceinline__ void wide_values(Warp<MXQ_MXFP4, D, NT>& w, const uint32_t (&p)[NT][2], const uint32_t (&sb)[2][D / 64],
                                             uint32_t unit) {

@@ -266,3 +266,19 @@ def test_pages_in_front_of_the_window_are_not_looked_at(orc, fmt, D, G, q):
         p.table[b, :first // 16] = -7
     out, lse = p.run(window=20)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("exp", range(-14, 4))
+def test_mxfp4_small_probabilities_of_small_values(orc, D, exp):
+    """A probability of about 2^-24 keeps 2^-28 of the largest one, whatever the values' scale, when a row's values are
+    all of that scale: two tokens, each with a value in a channel of its own."""
+    p = Problem("mxfp4", D, 1, 7, 16, [2], [1], seed=3)
+    k, v = torch.zeros((2, 1, D), dtype=torch.bfloat16), torch.zeros((2, 1, D), dtype=torch.bfloat16)
+    k[0, 0, 0] = -24.0
+    v[0, 0, 0] = v[1, 0, 1] = 2.0 ** exp
+    _rewrite(p, k, v)
+    p.q.zero_()
+    p.q[0, :, 0] = (0.9 + 0.03 * torch.arange(7)).to(torch.bfloat16)
+    out, lse = p.run(scale=LN2, out_dtype=torch.float32)
+    kh.check_attention(out, lse, p.ref(scale=LN2), "2^%d" % exp)
